@@ -584,8 +584,8 @@ def run(state):
         blocks = torch.empty(c["rows"], c["kv_heads"], c["top"], dtype=torch.int32, device="cuda")
         out = torch.empty_like(st["q"])
         lse = torch.empty(st["q"].shape[:2], dtype=torch.float32, device="cuda")
-        ibp.ibp_select_pages(st["q"], st["bounds"], st["k_table"], st["lens"], blocks, page_tokens=c["page"],
-                             keep_first=1, keep_last=2, row_seq=st["row_seq"])
+        ibp.ibp_select_pages(st["q"], st["bounds"], st["k_table"], st["lens"], blocks, meta=st["k"]["meta"],
+                             page_tokens=c["page"], keep_first=1, keep_last=2, row_seq=st["row_seq"])
         ibp.ibp_sparse_attention(st["k"]["pages"], st["v"]["pages"], st["q"], st["k_table"], st["v_table"],
                                  st["lens"], blocks, out, lse, scale=c["dim"] ** -0.5, row_seq=st["row_seq"])
         return blocks, out, lse
@@ -606,7 +606,7 @@ def run(state):
             return _plain_fork(st)
         pool = st["k"]
         ibp.ibp_pages_fork(pool["meta"], pool["slots"], pool["n"], pool["bitmask"], st["refs"], st["table"], st["lens"],
-                           st["parents"], st["children"])
+                           st["parents"], st["children"], page_tokens=c["page"])
         after = (st["table"][st["children"]], st["refs"].clone())
         ibp.ibp_pages_free(pool["meta"], st["refs"], pool["n"], st["table"], st["children"])
         return after + (st["refs"], st["table"], pool["slots"], pool["bitmask"])
