@@ -257,11 +257,179 @@ ibp_status ibp_gather_decompress_split(ibp_meta_t meta, const void* slots, uint6
                                        const uint32_t* headers, const uint32_t* bitmask, const int64_t* ids,
                                        uint64_t n_ids, void* dst, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Pages of a key/value cache.  A pool is fixed slots with their bitmask, as
+ * ibp_compress leaves them: a closed page may be a record (bit 1), the page
+ * that is still being filled is a raw slot (bit 0) that the caller writes in
+ * place.  A block table (device int64, row-major) holds the slot ids of a
+ * sequence's pages in order, -1 where there is none; refs (device int32, one
+ * per slot) counts who holds a page, 0 = free.
+ *
+ * The calls below need pages of at most 8 KiB that are a multiple of 16
+ * bytes, 16-byte aligned slots and at most 2^32 - 2 of them; otherwise they
+ * return IBP_ERR_UNSUPPORTED or IBP_ERR_INVALID_ARG.  None allocates memory
+ * or reads results on the host, so every one may be captured in a HIP graph;
+ * scratch comes from the caller (`workspace`, device, 8-byte aligned), and
+ * two calls that may overlap in time must not share it.  Ids that are neither
+ * -1 nor a slot latch IBP_ERR_RANGE.
+ * ------------------------------------------------------------------------- */
+
+/* The item of slot src_ids[i] (its record, or the whole raw page) and its
+ * bitmask bit -> slot dst_ids[i], without decoding; entries whose source or
+ * destination is -1 are skipped.  Only a record's bytes move, so pages go to
+ * and from pinned host memory at their compressed size; destination bytes
+ * past the item stay as they were.  The pools may be one (no destination may
+ * then be the source of another entry) or must not overlap; destinations
+ * must be distinct.  A record that is not valid is copied as a whole slot
+ * and latches IBP_ERR_CORRUPT. */
+ibp_status ibp_pages_copy(ibp_meta_t meta, const void* src_slots, uint64_t n_src, const uint32_t* src_bitmask,
+                          const int64_t* src_ids, void* dst_slots, uint64_t n_dst, uint32_t* dst_bitmask,
+                          const int64_t* dst_ids, uint64_t n, hipStream_t stream);
+
+/* Workspace bytes of the next calls: n = 0 for ibp_pages_alloc and
+ * ibp_pages_compact, forks * heads for ibp_pages_fork. */
+uint64_t ibp_pages_workspace(uint64_t n_slots, uint64_t n);
+
+/* ids[0..n) <- the n lowest free slots in ascending order, whose counts
+ * become 1.  With fewer free slots the rest of ids is -1 and IBP_ERR_NOMEM
+ * is latched. */
+ibp_status ibp_pages_alloc(ibp_meta_t meta, int32_t* refs, uint64_t n_slots, int64_t* ids, uint64_t n,
+                           void* workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+/* Sequence children[i] becomes a fork of sequence parents[i] (device int64,
+ * rows of table: n_seqs x n_heads x table_blocks ids): the lens[parent] /
+ * page_tokens full pages are shared (their counts grow by one), a partly
+ * filled page after them is copied into the lowest free slots, in the order
+ * of i and then of heads, and the rest of the child's row becomes -1.  The
+ * child's former row is overwritten, not released; lens is only read.
+ * Children must be distinct and no child a parent in the same call; a pair
+ * that is not valid latches IBP_ERR_RANGE and is left out, and a page for
+ * which no slot is free becomes -1 and latches IBP_ERR_NOMEM. */
+ibp_status ibp_pages_fork(ibp_meta_t meta, void* slots, uint64_t n_slots, uint32_t* bitmask, int32_t* refs,
+                          int64_t* table, uint64_t n_seqs, uint32_t n_heads, uint64_t table_blocks,
+                          const int32_t* lens, uint32_t page_tokens, const int64_t* parents, const int64_t* children,
+                          uint64_t n, void* workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+/* Every page in the rows of the given sequences is released (its count falls
+ * by one) and its entry becomes -1.  A count that is 0 already stays 0 and
+ * latches IBP_ERR_CORRUPT. */
+ibp_status ibp_pages_free(ibp_meta_t meta, int32_t* refs, uint64_t n_slots, int64_t* table, uint64_t n_seqs,
+                          uint32_t n_heads, uint64_t table_blocks, const int64_t* seqs, uint64_t n,
+                          hipStream_t stream);
+
+/* Moves the live pages (refs > 0) into slots [0, *n_live): the j-th free
+ * slot in front of n_live takes the j-th live page counted from the back,
+ * with its bit and count; the count it leaves is 0.  map (device int64,
+ * n_slots) receives each slot's new id (-1: it was free), n_live (device
+ * int64) the number of live pages, and the n_entries ids at table (may be
+ * NULL with 0) are rewritten through map. */
+ibp_status ibp_pages_compact(ibp_meta_t meta, void* slots, uint64_t n_slots, uint32_t* bitmask, int32_t* refs,
+                             int64_t* map, int64_t* n_live, int64_t* table, uint64_t n_entries, void* workspace,
+                             uint64_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention over the pages, read where they lie: a page of page_tokens x
+ * head_dim numbers (bf16 or fp16, row-major) of one key/value head is one
+ * slot, raw or a record, which the kernels rebuild on the way to the matrix
+ * cores.  head_dim 64, 128 or 256; page_tokens 16, 32 or 64 with pages of at
+ * most 8 KiB; anything else returns IBP_ERR_UNSUPPORTED.  Keys and values
+ * have a pool each (two handles, or one), a slot id each, in device or
+ * pinned memory.  n_q_heads is a multiple of n_kv_heads; query head h reads
+ * key/value head h / (n_q_heads / n_kv_heads).  All other data is device
+ * memory; strides are in numbers.
+ *
+ * Scores are scale * q.k in 32 bits, the softmax's maximum and sum are held
+ * in 32 bits, its weights are rounded to the data's type for the product
+ * with the values, which is summed in 32 bits.  A row that sees no key, or
+ * only keys whose score is -infinity, gives zeros and lse -infinity.  What
+ * lies in a page behind a sequence's last token, and keys and values that a
+ * row does not see, never reach its result, infinities and NaN included.
+ * ------------------------------------------------------------------------- */
+typedef enum ibp_dtype { IBP_BF16 = 0, IBP_FP16 = 1 } ibp_dtype;
+
+typedef struct ibp_pages {
+    ibp_meta_t meta;         /* L = page_tokens * head_dim * 2 */
+    const void* slots;       /* device or pinned, 16-byte aligned */
+    uint64_t n_slots;
+    const uint32_t* bitmask; /* device */
+} ibp_pages;
+
+typedef struct ibp_attention {
+    uint32_t dtype;          /* ibp_dtype of q, pages, k_new, v_new and out */
+    uint32_t head_dim;
+    uint32_t page_tokens;
+    uint32_t n_q_heads;
+    uint32_t n_kv_heads;
+    float scale;
+    uint64_t n_rows;         /* rows of q, out and lse */
+    uint64_t n_seqs;         /* rows of the block tables: n_seqs x n_kv_heads x table_blocks */
+    uint64_t table_blocks;
+    uint64_t max_len;        /* about the longest context: a hint, read to plan the split only */
+    uint32_t max_new;        /* most drafted tokens of a sequence (tree attention) */
+    int64_t q_row_stride, q_head_stride;
+    int64_t new_row_stride, new_head_stride; /* of k_new and v_new */
+} ibp_attention;
+
+/* Attention of a tree of drafted tokens.  Sequence s has lens[s] tokens in
+ * its pages and new_rows[s + 1] - new_rows[s] drafted ones (device int32,
+ * n_seqs + 1, ascending), whose queries, keys and values are those rows of
+ * q (n_q_heads x head_dim), k_new and v_new (n_kv_heads x head_dim).  A
+ * drafted token sees all of the context and drafted token j of its sequence
+ * where bit j % 64 of word j / 64 of its mask row (device uint64, n_rows x
+ * mask_words) is set: itself and its ancestors in a tree, any other pattern
+ * just as well.  Decoding one token is the tree of one node.
+ * out: n_rows x n_q_heads x head_dim; lse (may be NULL): n_rows x n_q_heads
+ * floats, the log of the softmax's sum.  Rows behind the last sequence's stay
+ * as they were.  A sequence with more than max_new or 64 * mask_words drafted
+ * tokens, or more context than its table row holds, latches IBP_ERR_RANGE
+ * and its rows are unspecified, as are those of corrupt pages
+ * (IBP_ERR_CORRUPT) and of table entries that are no slot (IBP_ERR_RANGE). */
+uint64_t ibp_tree_attention_workspace(const ibp_attention* a);
+ibp_status ibp_tree_attention(const ibp_pages* k, const ibp_pages* v, const ibp_attention* a, const void* q,
+                              const int64_t* k_table, const int64_t* v_table, const int32_t* lens,
+                              const int32_t* new_rows, const void* k_new, const void* v_new, const uint64_t* mask,
+                              uint32_t mask_words, void* out, float* lse, void* workspace, uint64_t workspace_bytes,
+                              hipStream_t stream);
+
+/* Bounds of pages: for i < n, bounds[ids[i]] (2 x head_dim numbers of the
+ * data's type) <- the smallest, then the largest, of each number over the
+ * first tokens[i] tokens (NULL: all) of page ids[i]; an id of -1 or no token
+ * at all is skipped, and a NaN is passed on.  With q these bound the score of
+ * every key in the page: sum over d of max(q_d lo_d, q_d hi_d). */
+ibp_status ibp_page_bounds(const ibp_pages* k, uint32_t dtype, uint32_t head_dim, const int64_t* ids,
+                           const int32_t* tokens, uint64_t n, void* bounds, hipStream_t stream);
+
+/* The pages that each query reads: row r of q belongs to sequence
+ * row_seq[r] (device int32; NULL: r) and sees its first lens[r] tokens, in
+ * nb = ceil(lens[r] / page_tokens) pages.  blocks (device int32, n_rows x
+ * n_kv_heads x n_blocks) receives block numbers in ascending order, -1 behind
+ * them: the first keep_first and the last keep_last of the nb, then those
+ * with the highest score until there are n_blocks.  A block's score is the
+ * highest of its bound over the query heads of the group, summed in 64 bits
+ * and rounded to 32; equal scores go to the lower block, and a NaN counts as
+ * the lowest.  bounds: pool-wide, as ibp_page_bounds leaves them, indexed by
+ * the ids of the keys' table.  At most 2^17 blocks per row.  Of a, max_len,
+ * max_new, scale and the new_ strides are not read. */
+uint64_t ibp_select_pages_workspace(const ibp_attention* a);
+ibp_status ibp_select_pages(ibp_meta_t meta, const ibp_attention* a, const void* q, const void* bounds,
+                            uint64_t n_slots, const int64_t* k_table, const int32_t* lens, const int32_t* row_seq,
+                            uint32_t keep_first, uint32_t keep_last, int32_t* blocks, uint32_t n_blocks,
+                            void* workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+/* Attention of each row over the blocks listed for it and its key/value head
+ * (blocks as ibp_select_pages writes them; -1 is skipped anywhere, a block
+ * listed twice counts twice), of which it sees tokens below lens[r]. */
+uint64_t ibp_sparse_attention_workspace(const ibp_attention* a, uint32_t n_blocks);
+ibp_status ibp_sparse_attention(const ibp_pages* k, const ibp_pages* v, const ibp_attention* a, const void* q,
+                                const int64_t* k_table, const int64_t* v_table, const int32_t* lens,
+                                const int32_t* row_seq, const int32_t* blocks, uint32_t n_blocks, void* out,
+                                float* lse, void* workspace, uint64_t workspace_bytes, hipStream_t stream);
+
 /* Waits for `stream`, returns the first error latched by a kernel of this
  * handle since the last ibp_check (IBP_OK if none) and clears it:
- * IBP_ERR_RANGE, IBP_ERR_CORRUPT, or IBP_ERR_DEVICE when a tile gave up
- * waiting for its predecessor in the look-back (its tensor's output is then
- * unspecified). */
+ * IBP_ERR_RANGE, IBP_ERR_CORRUPT, IBP_ERR_NOMEM when a page found no free
+ * slot, or IBP_ERR_DEVICE when a tile gave up waiting for its predecessor in
+ * the look-back (its tensor's output is then unspecified). */
 ibp_status ibp_check(ibp_meta_t meta, hipStream_t stream);
 
 const char* ibp_status_string(ibp_status status);

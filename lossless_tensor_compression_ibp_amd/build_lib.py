@@ -12,7 +12,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libibp.so")
-SOURCES = ["ibp_meta.hip", "ibp_encode.hip", "ibp_decode.hip", "ibp_api.hip"]
+SOURCES = ["ibp_meta.hip", "ibp_encode.hip", "ibp_decode.hip", "ibp_api.hip",
+           "ibp_pages.hip", "ibp_select.hip", "ibp_attention.hip", "ibp_attention_bf16.hip",
+           "ibp_attention_fp16.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -1,0 +1,647 @@
+// ibp_attention.hpp -- attention over a cache's pages: the kernels, for one
+// number type.  Each number type is compiled in a file of its own.
+//
+// Mathematics.  For the rows of one key/value head, t_j = scale * q.k_j,
+// o = sum_j exp(t_j - m) v_j / sum_j exp(t_j - m) with the running maximum m.
+// Both products run transposed, S^T = K Q^T and O^T = V^T P^T: a lane of the
+// matrix cores' result then holds four tokens (S^T) or four dims (O^T) of ONE
+// row, its column l % 16, so m, the sum and the rescaling are one number per
+// lane, and the weights that a lane computes from S^T are exactly the eight it
+// has to supply to O^T's product: tokens 4 g + 0..3 of two tiles of 16, where
+// g = l / 16.  (The product sums over tokens, so their order is free as long
+// as V^T's operand has the same: two transposed LDS reads of four tokens.)
+//
+// Pages.  A wave loads a slot linearly (16 bytes per lane and instruction),
+// rebuilds it in registers if it holds a record, and writes it to LDS as rows
+// of tokens, padded so that the operand reads spread over the banks.  The next
+// page's loads are in flight meanwhile.
+//
+// Two shapes of work:
+//   SHARED = false: few rows (16 MR).  Every wave walks pages of its own for
+//     all rows, without a barrier, and the waves' results are joined at the
+//     end.  Bound by the pages' bytes (or their rebuild).
+//   SHARED = true: many rows.  The workgroup's waves load a step's pages
+//     together, each rebuilding its share, and each multiplies all of them
+//     with 16 MR rows of its own.
+// A long context is split over workgroups; k_join adds the parts.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ibp_kv_math.hpp"
+
+namespace ibp {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kAttnWaves = 4;
+
+struct AttnArgs {
+    Pool k, v;
+    const uint16_t* q;
+    const int64_t* k_table;
+    const int64_t* v_table;
+    const int32_t* lens;
+    const int32_t* new_rows;   // tree
+    const uint16_t* k_new;
+    const uint16_t* v_new;
+    const uint32_t* mask;      // tree: 2 * mask_words per row
+    const int32_t* row_seq;    // sparse
+    const int32_t* blocks;     // sparse: n_list per (row, head)
+    uint16_t* out;
+    float* lse;
+    float* part;               // [row][head][split][D], then [row][head][split][2]
+    float* part_ml;
+    uint64_t n_rows, n_seqs, table_blocks;
+    int64_t q_row, q_head, new_row, new_head;
+    uint32_t n_list, mask_words2, max_new;
+    uint32_t kv_heads, group, splits, row_tiles, work;  // work: (sequence or row) * kv_heads
+    uint32_t q_vec, new_vec;
+    uint32_t tab_words_k, tab_words_v;  // LDS words of the tables (0: not staged)
+    uint32_t tab_lds_k, tab_lds_v;      // staged in LDS, else read where they lie in device memory
+    uint32_t same_tab;                  // values have the keys' tables
+    float scale2;              // scale * log2(e)
+};
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+// Four tokens' numbers of one dim: within 16 lanes, lane i addresses four
+// consecutive dims of token i / 4 and receives dim i of the four tokens.
+__device__ __forceinline__ u32x2 read_transposed(const char* lds) {
+    typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)lds));
+}
+
+template <int D, int T, bool SHARED>
+struct AttnShape {
+    static constexpr int NV = D * T / 512;                 // vectors per lane of a page
+    static constexpr int STEP = SHARED ? (T == 64 ? 128 : 64) : (T < 32 ? 32 : T);
+    static constexpr int PP = STEP / T;                    // pages per step
+    static constexpr bool BOTH = !SHARED || T == 16;       // a wave loads keys and values
+    static constexpr int PW = SHARED ? 1 : PP;             // pages per step, wave and kind
+    static constexpr int RK = 2 * D + 16, RV = 2 * D + 32; // bytes per token row in LDS
+    static constexpr uint32_t stage_bytes = 4 * page_stage_words<NV>();
+    static constexpr int CHUNK = SHARED ? 64 : STEP;       // tokens per pass of the softmax
+    static constexpr bool ONE = !SHARED && PW * NV > 8;    // one register buffer for keys and values in turn
+    static constexpr uint32_t wave_bytes = (stage_bytes + 15) / 16 * 16 + (SHARED ? 0 : STEP * RV);
+    static constexpr uint32_t shared_bytes = SHARED ? STEP * (RK + RV) : 0;
+    static constexpr uint32_t join_bytes = SHARED ? 0 : kAttnWaves * (16 * (D + 4) * 4);
+    static constexpr uint32_t area_bytes =
+        kAttnWaves * wave_bytes + shared_bytes > join_bytes ? kAttnWaves * wave_bytes + shared_bytes : join_bytes;
+};
+
+__device__ __forceinline__ void lds_order() { asm volatile("" ::: "memory"); }
+
+template <class E, int D, int T, int MR, bool SHARED, bool TREE>
+__global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
+    using S = AttnShape<D, T, SHARED>;
+    using V8 = typename E::V8;
+    constexpr int NV = S::NV, STEP = S::STEP, PP = S::PP, PW = S::PW, TILES = S::CHUNK / 16;
+    constexpr int DK = D / 32, DN = D / 16;
+    extern __shared__ uint32_t smem[];
+    __shared__ float join_m[kAttnWaves][16], join_l[kAttnWaves][16];
+    const uint32_t lane = lane_id(), wib = uniform(threadIdx.x / kWave);
+    const uint32_t col = lane & 15u, g = lane >> 4;
+
+    // which part of the work: split, (sequence or row, head), row tile
+    const uint32_t split = blockIdx.x % a.splits;
+    const uint32_t wg = (blockIdx.x / a.splits) % a.work, rt = blockIdx.x / a.splits / a.work;
+    const uint32_t h = wg % a.kv_heads;
+    const uint64_t item = wg / a.kv_heads;  // sequence (tree) or row
+    int64_t seq = TREE ? (int64_t)item : (a.row_seq ? (int64_t)a.row_seq[item] : (int64_t)item);
+    int64_t len = a.lens[item];
+    uint64_t first_row = TREE ? 0 : item;
+    uint32_t n_new = TREE ? 0 : 1;
+    bool bad = seq < 0 || (uint64_t)seq >= a.n_seqs || len < 0;
+    if (TREE) {
+        const int64_t r0 = a.new_rows[item], r1 = a.new_rows[item + 1];
+        if (r0 < 0 || r1 < r0 || (uint64_t)r1 > a.n_rows || r1 - r0 > (int64_t)a.max_new ||
+            (uint64_t)(r1 - r0) > 32ull * a.mask_words2) {
+            bad = true;
+        } else {
+            first_row = (uint64_t)r0;
+            n_new = (uint32_t)(r1 - r0);
+        }
+    }
+    if (!bad && (uint64_t)len > a.table_blocks * T) bad = true;
+    if (bad) {
+        latch_error(a.k.err, kErrRange);
+        if (TREE) return;
+        seq = 0;
+        len = 0;
+    }
+    const uint32_t rows = n_new * a.group;
+    constexpr uint32_t kRowsWg = 16u * MR * (SHARED ? kAttnWaves : 1u);
+    if (rt * kRowsWg >= rows) return;
+    const uint32_t row0 = rt * kRowsWg + (SHARED ? wib * 16u * MR : 0u);
+
+    // steps of this split: the context's, then the drafted tokens'
+    const uint32_t ctx_pages = TREE ? (uint32_t)((len + T - 1) / T) : (len > 0 ? a.n_list : 0u);
+    const uint32_t ctx_steps = (ctx_pages + PP - 1) / PP;
+    const uint32_t all_steps = ctx_steps + (TREE ? (n_new + STEP - 1) / STEP : 0u);
+    const uint32_t per = (all_steps + a.splits - 1) / a.splits;
+    const uint32_t s_lo = min(split * per, all_steps), s_hi = min(s_lo + per, all_steps);
+    const uint32_t s_first = s_lo + (SHARED ? 0u : wib);
+    constexpr uint32_t kStride = SHARED ? 1u : kAttnWaves;
+    const uint32_t n_steps = s_first < s_hi ? (s_hi - s_first + kStride - 1) / kStride : 0u;
+
+    // tables of the record formats
+    if (a.tab_lds_k) stage_page_tables(a.k, smem);
+    if (a.tab_lds_v && !a.same_tab) stage_page_tables(a.v, smem + a.tab_words_k);
+    __syncthreads();
+    char* const area = reinterpret_cast<char*>(smem + a.tab_words_k + a.tab_words_v);
+    uint32_t* const stage = reinterpret_cast<uint32_t*>(area + wib * S::wave_bytes);
+    char* const k_tile =
+        SHARED ? area + kAttnWaves * S::wave_bytes : reinterpret_cast<char*>(stage) + (S::stage_bytes + 15) / 16 * 16;
+    char* const v_tile = SHARED ? k_tile + STEP * S::RK : k_tile;
+
+    // a wave of SHARED pages of 32 or 64 tokens loads keys or values only
+    const bool only_v = !S::BOTH && (wib & 1u);
+    const uint32_t page_in_step = SHARED ? (T == 16 ? wib : wib >> 1) : 0u;
+
+    // --- the wave's next pages: lane l has page l % PW of its step base + l / PW
+    uint32_t id_a = kNoPage, id_b = kNoPage, held = 0, comp = 0;
+    const int32_t* list = TREE ? nullptr : a.blocks + (item * a.kv_heads + h) * a.n_list;
+    const uint64_t table_row = ((uint64_t)seq * a.kv_heads + h) * a.table_blocks;
+    auto refill = [&](uint32_t base) __attribute__((always_inline)) {
+        const uint32_t s = s_first + (base + lane / PW) * kStride;
+        id_a = id_b = kNoPage;
+        held = comp = 0;
+        if (s < s_hi && s < ctx_steps) {
+            const uint32_t n = s * PP + (SHARED ? page_in_step : lane % PW);
+            int64_t block = n < ctx_pages ? (TREE ? (int64_t)n : (int64_t)list[n]) : -1;
+            if (block >= 0 && block * T < len) {
+                held = (uint32_t)min((int64_t)T, len - block * T);
+                bool missing = false;
+                if (S::BOTH || !only_v) {
+                    id_a = page_id(a.k_table[table_row + block], a.k.n_slots);
+                    missing = id_a == kNoPage;
+                    if (!missing) comp = page_bit(a.k.bitmask, id_a);
+                }
+                if (S::BOTH || only_v) {
+                    const uint32_t id = page_id(a.v_table[table_row + block], a.v.n_slots);
+                    missing |= id == kNoPage;
+                    const uint32_t bit = id == kNoPage ? 0u : page_bit(a.v.bitmask, id);
+                    if (S::BOTH) {
+                        id_b = id;
+                        comp |= bit << 1;
+                    } else {
+                        id_a = id;
+                        comp = bit;
+                    }
+                }
+                if (missing) atomicCAS(a.k.err, 0u, (uint32_t)kErrRange);
+            }
+        }
+    };
+    // page p of local step i -> registers; draft steps read the dense rows
+    auto load = [&](u32x4* st, uint32_t i, bool values, uint32_t slot_lo) __attribute__((always_inline)) {
+        const uint32_t s = s_first + i * kStride;
+#pragma unroll
+        for (int p = 0; p < PW; ++p) {
+            u32x4* dst = st + p * NV;
+            if (TREE && s >= ctx_steps) {
+                const uint32_t j0 = (s - ctx_steps) * STEP + (SHARED ? page_in_step : (uint32_t)p) * T;
+                const uint16_t* base = (values ? a.v_new : a.k_new) + (int64_t)h * a.new_head;
+#pragma unroll
+                for (int r = 0; r < NV; ++r) {
+                    const uint32_t w = 256u * r + 4u * lane, token = j0 + w / (D / 2), d = 2 * (w % (D / 2));
+                    dst[r] = u32x4{0u, 0u, 0u, 0u};
+                    if (token < n_new)
+                        dst[r] = load_eight(base + (int64_t)(first_row + token) * a.new_row + d, a.new_vec != 0);
+                }
+            } else {
+                load_page<NV>(dst, values ? a.v.slots : a.k.slots,
+                              lane_value(slot_lo, (int)((i % (64 / PW)) * PW + p)));
+            }
+        }
+    };
+    // Page p of the wave as rows of tokens in LDS, rebuilt if it is a record;
+    // values behind its last token become zero.
+    auto put = [&](const u32x4* st, int p, bool values, bool record, uint32_t n, char* tile, int stride)
+                   __attribute__((always_inline)) {
+        char* const to = tile + (SHARED ? page_in_step : (uint32_t)p) * (T * stride);
+        const uint32_t keep = values ? n : (uint32_t)T;
+        auto sink = [&](uint32_t w, u32x4 x) __attribute__((always_inline)) {
+            const uint32_t token = w / (D / 2), b = 4 * (w % (D / 2));
+            if (token >= keep) x = u32x4{0u, 0u, 0u, 0u};
+            *reinterpret_cast<u32x4*>(to + token * stride + b) = x;
+        };
+        if (record) {
+            const Pool& pool = values ? a.v : a.k;
+            bool ok;
+            if (values ? a.tab_lds_v : a.tab_lds_k)
+                ok = rebuild_page<NV>(st, pool, page_tab(pool, smem + (values && !a.same_tab ? a.tab_words_k : 0u)),
+                                      stage, sink);
+            else
+                ok = rebuild_page<NV>(st, pool, page_tab_global(pool), stage, sink);
+            if (!ok) latch_error(pool.err, kErrCorrupt);
+        } else {
+#pragma unroll
+            for (int r = 0; r < NV; ++r) sink(256u * r + 4u * lane, st[r]);
+        }
+    };
+
+    // --- the rows' queries (B operand) and running state
+    V8 qf[MR][DK];
+    float m[MR], l[MR];
+    f32x4 o[MR][DN];
+    uint64_t q_row[MR];
+    bool q_on[MR];
+#pragma unroll
+    for (int t = 0; t < MR; ++t) {
+        const uint32_t rho = row0 + 16 * t + col;
+        q_on[t] = rho < rows;
+        const uint32_t i = rho / a.group, j = rho - i * a.group;
+        q_row[t] = first_row + (q_on[t] ? i : 0u);
+        const uint16_t* qp = a.q + (int64_t)q_row[t] * a.q_row + (int64_t)(h * a.group + j) * a.q_head;
+#pragma unroll
+        for (int kk = 0; kk < DK; ++kk) {
+            const u32x4 x = q_on[t] ? load_eight(qp + 32 * kk + 8 * g, a.q_vec != 0) : u32x4{0u, 0u, 0u, 0u};
+            qf[t][kk] = bits_as<V8>(x);
+        }
+        m[t] = -__builtin_inff();
+        l[t] = 0.f;
+#pragma unroll
+        for (int n = 0; n < DN; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    u32x4 st_a[PW * NV], st_b[S::BOTH && !S::ONE ? PW * NV : 1];
+    if (n_steps) {
+        refill(0);
+        load(st_a, 0, only_v, id_a);
+        if (S::BOTH && !S::ONE) load(st_b, 0, true, id_b);
+    }
+    for (uint32_t i = 0; i < n_steps; ++i) {
+        const uint32_t s = s_first + i * kStride;
+        const bool draft = TREE && s >= ctx_steps;
+        // tokens held by each page that this wave loads, and what is a record
+        uint32_t n_held[PW], c_held[PW];
+#pragma unroll
+        for (int p = 0; p < PW; ++p) {
+            const int at = (int)((i % (64 / PW)) * PW + p);
+            n_held[p] = lane_value(held, at);
+            c_held[p] = lane_value(comp, at);
+            if (draft) {
+                const uint32_t j0 = (s - ctx_steps) * STEP + (SHARED ? page_in_step : (uint32_t)p) * T;
+                n_held[p] = n_new > j0 ? min(n_new - j0, (uint32_t)T) : 0u;
+                c_held[p] = 0;
+            }
+        }
+        auto process = [&](const u32x4* st, bool values, uint32_t bit, char* tile, int stride) __attribute__((
+                           always_inline)) {
+            lds_order();
+#pragma unroll
+            for (int p = 0; p < PW; ++p)
+                put(st + p * NV, p, values, ((c_held[p] >> bit) & 1u) != 0, n_held[p], tile, stride);
+            lds_order();
+        };
+        const bool more = i + 1 < n_steps;
+        const uint32_t this_b = id_b;
+        uint32_t next_b = kNoPage;
+        auto advance = [&]() __attribute__((always_inline)) {
+            if (more && (i + 1) % (64 / PW) == 0) refill(i + 1);
+            next_b = id_b;
+        };
+        if constexpr (SHARED) {
+            __syncthreads();  // the tiles are free
+            if (S::BOTH) {
+                process(st_a, false, 0, k_tile, S::RK);
+                process(st_b, true, 1, v_tile, S::RV);
+            } else if (only_v) {
+                process(st_a, true, 0, v_tile, S::RV);
+            } else {
+                process(st_a, false, 0, k_tile, S::RK);
+            }
+            advance();
+            if (more) {
+                load(st_a, i + 1, only_v, id_a);
+                if (S::BOTH) load(st_b, i + 1, true, next_b);
+            }
+            __syncthreads();
+        } else {
+            process(st_a, false, 0, k_tile, S::RK);
+            if constexpr (S::ONE) {
+                load(st_a, i, true, this_b);
+                advance();
+            } else {
+                advance();
+                if (more) load(st_a, i + 1, false, id_a);
+            }
+        }
+
+#pragma unroll 1
+        for (uint32_t c = 0; c < (uint32_t)(STEP / S::CHUNK); ++c) {
+        // valid tokens of each tile of 16
+        const uint32_t t0 = c * S::CHUNK;
+        uint32_t step_held = 0;
+        if (SHARED || TREE) {
+            const int64_t n = draft ? (int64_t)n_new - (int64_t)(s - ctx_steps) * STEP : len - (int64_t)s * STEP;
+            step_held = (uint32_t)max(min(n, (int64_t)STEP) - (int64_t)t0, (int64_t)0);
+        }
+        auto tile_held = [&](int u) __attribute__((always_inline)) -> uint32_t {
+            if constexpr (TREE || SHARED) {
+                return step_held > 16u * u ? step_held - 16u * u : 0u;
+            } else {
+                const uint32_t n = n_held[(u * 16) / T < PW ? (u * 16) / T : 0];
+                return n > (uint32_t)(u * 16 % T) ? n - (uint32_t)(u * 16 % T) : 0u;
+            }
+        };
+
+        const char* const kt = k_tile + t0 * S::RK;
+        const char* const vt = v_tile + t0 * S::RV;
+        // S^T = K Q^T
+        f32x4 sc[MR][TILES];
+#pragma unroll
+        for (int u = 0; u < TILES; ++u) {
+#pragma unroll
+            for (int t = 0; t < MR; ++t) sc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kk = 0; kk < DK; ++kk) {
+                const V8 kf =
+                    *reinterpret_cast<const V8*>(kt + (16 * u + col) * S::RK + 64 * kk + 16 * g);
+#pragma unroll
+                for (int t = 0; t < MR; ++t) sc[t][u] = E::mfma(kf, qf[t][kk], sc[t][u]);
+            }
+        }
+        // scaled scores, masked ones -infinity; bit 4 u + e of `seen` (drafts)
+        bool whole = !draft;
+#pragma unroll
+        for (int u = 0; u < TILES; ++u) whole = whole && tile_held(u) >= 16u;
+#pragma unroll
+        for (int t = 0; t < MR; ++t) {
+            uint32_t seen[(TILES + 1) / 2];
+            if (draft) {
+#pragma unroll
+                for (int w = 0; w < (TILES + 1) / 2; ++w) {
+                    const uint32_t word = (s - ctx_steps) * (STEP / 32) + t0 / 32 + w;
+                    seen[w] = q_on[t] && word < a.mask_words2 ? a.mask[q_row[t] * a.mask_words2 + word] : 0u;
+                }
+            }
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int u = 0; u < TILES; ++u) {
+                const uint32_t n = tile_held(u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = sc[t][u][e] * a.scale2;
+                    if (!whole) {
+                        bool on = 4 * g + e < n;
+                        if (draft) on = on && ((seen[u >> 1] >> (16 * (u & 1) + 4 * g + e)) & 1u);
+                        x = on ? x : -__builtin_inff();
+                    }
+                    sc[t][u][e] = x;
+                    top = fmaxf(top, x);
+                }
+            }
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            // The maximum is moved only when a score passes it by more than
+            // 8 (weights then stay below 2^8 and sums far from overflow), so
+            // most steps rescale nothing.
+            if (ballot(top > m[t] + 8.f || (m[t] == -__builtin_inff() && top != -__builtin_inff()))) {
+                const float m_new = fmaxf(m[t], top);
+                const float f = m_new == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(m[t] - m_new);
+                m[t] = m_new;
+                l[t] *= f;
+#pragma unroll
+                for (int n = 0; n < DN; ++n) o[t][n] *= f;
+            }
+            const float base = m[t] == -__builtin_inff() ? 0.f : m[t];
+#pragma unroll
+            for (int u = 0; u < TILES; ++u) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float p = __builtin_amdgcn_exp2f(sc[t][u][e] - base);
+                    sc[t][u][e] = p;
+                    l[t] += p;
+                }
+            }
+        }
+
+        // O^T += V^T P^T
+        if constexpr (S::ONE) {
+            process(st_a, true, 1, v_tile, S::RV);
+            if (more) load(st_a, i + 1, false, id_a);
+        } else if constexpr (!SHARED) {
+            process(st_b, true, 1, v_tile, S::RV);
+            if (more) load(st_b, i + 1, true, next_b);
+        }
+        // A drafted value that is infinite or NaN must not reach the rows that
+        // do not see its token through a product with zero: such a step is
+        // summed token by token, over the tokens that a row sees.
+        bool odd = false;
+        if (draft) {
+            for (uint32_t w = lane; w < S::CHUNK * (D / 2); w += kWave) {
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(vt + (w / (D / 2)) * S::RV + 4 * (w % (D / 2)));
+                odd |= (x & E::kExponent) == E::kExponent || ((x >> 16) & E::kExponent) == E::kExponent;
+            }
+            odd = ballot(odd) != 0;
+        }
+        if (TREE && odd) {
+#pragma unroll
+            for (int t = 0; t < MR; ++t) {
+#pragma unroll
+                for (int u = 0; u < TILES; ++u) {
+                    const uint32_t word = (s - ctx_steps) * (STEP / 32) + t0 / 32 + (u >> 1);
+                    const uint32_t vis = q_on[t] && word < a.mask_words2
+                                             ? a.mask[q_row[t] * a.mask_words2 + word] >> (16 * (u & 1))
+                                             : 0u;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+#pragma unroll 1
+                        for (uint32_t gs = 0; gs < 4; ++gs) {
+                            const uint32_t token = 4 * gs + e;
+                            const float p = __shfl(sc[t][u][e], (int)(16 * gs + col));
+                            const bool on = ((vis >> token) & 1u) && token < tile_held(u);
+#pragma unroll
+                            for (int n = 0; n < DN; ++n) {
+                                const u32x2 x = *reinterpret_cast<const u32x2*>(
+                                    vt + (16 * u + token) * S::RV + 32 * n + 8 * g);
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    if (on) o[t][n][c] += p * E::from_bits(x[c >> 1] >> (16 * (c & 1)));
+                            }
+                        }
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < TILES; u += 2) {
+                V8 pf[MR];
+#pragma unroll
+                for (int t = 0; t < MR; ++t) {
+                    const u32x4 x = {E::pack(sc[t][u][0], sc[t][u][1]), E::pack(sc[t][u][2], sc[t][u][3]),
+                                     E::pack(sc[t][u + 1][0], sc[t][u + 1][1]),
+                                     E::pack(sc[t][u + 1][2], sc[t][u + 1][3])};
+                    pf[t] = bits_as<V8>(x);
+                }
+                const char* vp = vt + (16 * u + 4 * g + (col >> 2)) * S::RV + 8 * (col & 3);
+#pragma unroll
+                for (int n = 0; n < DN; ++n) {
+                    const u32x2 x = read_transposed(vp + 32 * n), y = read_transposed(vp + 16 * S::RV + 32 * n);
+                    const V8 vf = bits_as<V8>(u32x4{x[0], x[1], y[0], y[1]});
+#pragma unroll
+                    for (int t = 0; t < MR; ++t) o[t][n] = E::mfma(vf, pf[t], o[t][n]);
+                }
+            }
+        }
+        lds_order();
+        }
+    }
+
+    // --- the sums over the four lanes of a row, then the result or this split's part
+    const uint32_t nq = a.kv_heads * a.group;
+    auto finish = [&](uint64_t row, uint32_t head, uint32_t d, f32x4 x, float mm, float ll) __attribute__((
+                      always_inline)) {
+        const uint64_t rh = row * nq + head;
+        if (a.splits == 1) {
+            const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
+            const u32x2 y = {E::pack(x[0] * inv, x[1] * inv), E::pack(x[2] * inv, x[3] * inv)};
+            *reinterpret_cast<u32x2*>(a.out + rh * D + d) = y;
+            if (d == 0 && a.lse)
+                a.lse[rh] = ll > 0.f || ll != ll ? (mm + __builtin_amdgcn_logf(ll)) * kLn2 : -__builtin_inff();
+        } else {
+            *reinterpret_cast<f32x4*>(a.part + (rh * a.splits + split) * D + d) = x;
+            if (d == 0) {
+                a.part_ml[(rh * a.splits + split) * 2] = mm;
+                a.part_ml[(rh * a.splits + split) * 2 + 1] = ll;
+            }
+        }
+    };
+#pragma unroll
+    for (int t = 0; t < MR; ++t) {
+        l[t] += __shfl_xor(l[t], 16);
+        l[t] += __shfl_xor(l[t], 32);
+        if constexpr (SHARED) {
+            if (q_on[t]) {
+                const uint32_t rho = row0 + 16 * t + col, j = rho % a.group;
+#pragma unroll
+                for (int n = 0; n < DN; ++n) finish(q_row[t], h * a.group + j, 16 * n + 4 * g, o[t][n], m[t], l[t]);
+            }
+        } else {
+            // the waves' rows joined through LDS: [wave][row][D + 4]
+            float* const buf = reinterpret_cast<float*>(area);
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < DN; ++n)
+                *reinterpret_cast<f32x4*>(buf + (wib * 16 + col) * (D + 4) + 16 * n + 4 * g) = o[t][n];
+            if (g == 0) {
+                join_m[wib][col] = m[t];
+                join_l[wib][col] = l[t];
+            }
+            __syncthreads();
+            for (uint32_t e = threadIdx.x; e < 16 * (D / 4); e += kWave * kAttnWaves) {
+                const uint32_t c = e / (D / 4), d = 4 * (e % (D / 4));
+                const uint32_t rho = row0 + 16 * t + c;
+                if (rho >= rows) continue;
+                float mm = -__builtin_inff(), ll = 0.f;
+#pragma unroll
+                for (uint32_t w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, join_m[w][c]);
+                const float base = mm == -__builtin_inff() ? 0.f : mm;
+                f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (uint32_t w = 0; w < kAttnWaves; ++w) {
+                    const float f = __builtin_amdgcn_exp2f(join_m[w][c] - base);
+                    ll += f * join_l[w][c];
+                    x += f * *reinterpret_cast<const f32x4*>(buf + (w * 16 + c) * (D + 4) + d);
+                }
+                const uint32_t i = rho / a.group, j = rho - i * a.group;
+                finish(first_row + i, h * a.group + j, d, x, mm, ll);
+            }
+        }
+    }
+}
+
+// The splits' parts joined: D / 4 lanes per (row, head).
+template <class E, int D>
+__global__ __launch_bounds__(256) void k_join(AttnArgs a) {
+    const uint32_t nq = a.kv_heads * a.group;
+    const uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+    const uint64_t rh = e / (D / 4);
+    const uint32_t d = 4 * (uint32_t)(e % (D / 4));
+    uint64_t rows = a.n_rows;
+    if (a.new_rows) {
+        const int64_t last = a.new_rows[a.n_seqs];
+        rows = last < 0 ? 0 : min(rows, (uint64_t)last);
+    }
+    if (rh >= rows * nq) return;
+    if (a.new_rows && a.new_rows[0] > 0 && rh < (uint64_t)a.new_rows[0] * nq) return;
+    const float* ml = a.part_ml + rh * a.splits * 2;
+    const float* part = a.part + rh * a.splits * D + d;
+    float mm = -__builtin_inff(), ll = 0.f;
+    for (uint32_t s = 0; s < a.splits; ++s) mm = fmaxf(mm, ml[2 * s]);
+    const float base = mm == -__builtin_inff() ? 0.f : mm;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    for (uint32_t s = 0; s < a.splits; ++s) {
+        const float f = __builtin_amdgcn_exp2f(ml[2 * s] - base);
+        ll += f * ml[2 * s + 1];
+        x += f * *reinterpret_cast<const f32x4*>(part + (uint64_t)s * D);
+    }
+    const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
+    const u32x2 y = {E::pack(x[0] * inv, x[1] * inv), E::pack(x[2] * inv, x[3] * inv)};
+    *reinterpret_cast<u32x2*>(a.out + rh * D + d) = y;
+    if (d == 0 && a.lse) a.lse[rh] = ll > 0.f || ll != ll ? (mm + __builtin_amdgcn_logf(ll)) * kLn2 : -__builtin_inff();
+}
+
+// Shape of a launch, chosen by the host (plan_attention).
+struct AttnPlan {
+    int mr = 1;              // tiles of 16 rows per wave
+    bool shared = false;
+    uint32_t step = 0;       // tokens per step
+    uint32_t area_bytes = 0; // LDS besides the tables
+    uint32_t row_tiles = 1, splits = 1;
+};
+
+hipError_t launch_attention_bf16(const AttnArgs& a, const AttnPlan& p, uint32_t head_dim, uint32_t page_tokens,
+                                 bool tree, uint32_t lds, hipStream_t s);
+hipError_t launch_attention_fp16(const AttnArgs& a, const AttnPlan& p, uint32_t head_dim, uint32_t page_tokens,
+                                 bool tree, uint32_t lds, hipStream_t s);
+
+template <class E, int D, int T, int MR, bool SHARED, bool TREE>
+static hipError_t launch_attend(const AttnArgs& a, uint32_t lds, hipStream_t s) {
+    if (lds > kMaxLdsPerBlock) {  // more than 64 KiB has to be asked for
+        const hipError_t e =
+            hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend<E, D, T, MR, SHARED, TREE>),
+                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((k_attend<E, D, T, MR, SHARED, TREE>), dim3(a.splits * a.work * a.row_tiles),
+                       dim3(kWave * kAttnWaves), lds, s, a);
+    return hipGetLastError();
+}
+
+template <class E, int D, int T>
+static hipError_t launch_attention_t(const AttnArgs& a, const AttnPlan& p, bool tree, uint32_t lds, hipStream_t s) {
+    hipError_t e;
+    constexpr int M2 = D <= 128 ? 2 : 1;  // 32 rows of 256 dims would not leave registers for two waves per SIMD
+    if (!tree)
+        e = p.mr == 1 ? launch_attend<E, D, T, 1, false, false>(a, lds, s)
+                      : launch_attend<E, D, T, M2, false, false>(a, lds, s);
+    else if (!p.shared)
+        e = p.mr == 1 ? launch_attend<E, D, T, 1, false, true>(a, lds, s)
+                      : launch_attend<E, D, T, M2, false, true>(a, lds, s);
+    else
+        e = p.mr == 1 ? launch_attend<E, D, T, 1, true, true>(a, lds, s)
+                      : launch_attend<E, D, T, M2, true, true>(a, lds, s);
+    if (e != hipSuccess || a.splits == 1) return e;
+    const uint64_t threads = a.n_rows * a.kv_heads * a.group * (D / 4);
+    hipLaunchKernelGGL((k_join<E, D>), dim3((uint32_t)((threads + 255) / 256)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <class E>
+static hipError_t launch_attention_e(const AttnArgs& a, const AttnPlan& p, uint32_t head_dim, uint32_t page_tokens,
+                                     bool tree, uint32_t lds, hipStream_t s) {
+    if (head_dim == 64 && page_tokens == 16) return launch_attention_t<E, 64, 16>(a, p, tree, lds, s);
+    if (head_dim == 64 && page_tokens == 32) return launch_attention_t<E, 64, 32>(a, p, tree, lds, s);
+    if (head_dim == 64 && page_tokens == 64) return launch_attention_t<E, 64, 64>(a, p, tree, lds, s);
+    if (head_dim == 128 && page_tokens == 16) return launch_attention_t<E, 128, 16>(a, p, tree, lds, s);
+    if (head_dim == 128 && page_tokens == 32) return launch_attention_t<E, 128, 32>(a, p, tree, lds, s);
+    if (head_dim == 256 && page_tokens == 16) return launch_attention_t<E, 256, 16>(a, p, tree, lds, s);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace ibp

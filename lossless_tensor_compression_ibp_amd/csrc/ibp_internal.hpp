@@ -148,7 +148,7 @@ inline uint64_t encode_status_words(const Geo& g, uint64_t n_tensors) {
 // in `bits` (in place; gpt consecutive groups per tensor).
 hipError_t launch_group_scan(uint64_t n_tensors, uint64_t gpt, uint64_t base, uint64_t* bits, hipStream_t s);
 
-enum DeviceError : uint32_t { kErrNone = 0, kErrCorrupt = 5, kErrRange = 6, kErrStall = 7 };
+enum DeviceError : uint32_t { kErrNone = 0, kErrCorrupt = 5, kErrRange = 6, kErrStall = 7, kErrFull = 8 };
 
 // Where tensor t's stored item lives.  offsets == nullptr: fixed slots, slot
 // t at byte t * L.  Otherwise the packed cache layout: item t spans bytes

@@ -37,6 +37,9 @@ ABI_FUNCTIONS = (
     "ibp_packed_offsets", "ibp_compress_packed", "ibp_decompress_packed", "ibp_gather_decompress_packed",
     "ibp_compress_split", "ibp_decompress_split", "ibp_gather_decompress_split",
     "ibp_decompress_noalloc",
+    "ibp_pages_copy", "ibp_pages_workspace", "ibp_pages_alloc", "ibp_pages_fork", "ibp_pages_free",
+    "ibp_pages_compact", "ibp_tree_attention_workspace", "ibp_tree_attention", "ibp_page_bounds",
+    "ibp_select_pages_workspace", "ibp_select_pages", "ibp_sparse_attention_workspace", "ibp_sparse_attention",
 )
 
 
@@ -48,6 +51,20 @@ class ibp_params(ctypes.Structure):
 class ibp_meta_info(ctypes.Structure):
     _fields_ = [("invariant_bits", ctypes.c_uint64), ("min_record_bytes", ctypes.c_uint64),
                 ("max_runs", ctypes.c_uint32), ("uniform", ctypes.c_uint32)]
+
+
+class ibp_pages(ctypes.Structure):
+    _fields_ = [("meta", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("n_slots", ctypes.c_uint64),
+                ("bitmask", ctypes.c_void_p)]
+
+
+class ibp_attention(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_uint32), ("head_dim", ctypes.c_uint32), ("page_tokens", ctypes.c_uint32),
+                ("n_q_heads", ctypes.c_uint32), ("n_kv_heads", ctypes.c_uint32), ("scale", ctypes.c_float),
+                ("n_rows", ctypes.c_uint64), ("n_seqs", ctypes.c_uint64), ("table_blocks", ctypes.c_uint64),
+                ("max_len", ctypes.c_uint64), ("max_new", ctypes.c_uint32), ("q_row_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("new_row_stride", ctypes.c_int64),
+                ("new_head_stride", ctypes.c_int64)]
 
 
 class IBPError(RuntimeError):
@@ -87,11 +104,25 @@ def lib():
         L.ibp_compress_split.argtypes = [p, p, u64, p, p, p, p, p]
         L.ibp_decompress_split.argtypes = [p, p, p, p, u64, p, p]
         L.ibp_gather_decompress_split.argtypes = [p, p, u64, p, p, p, u64, p, p]
+        u32, A, G = ctypes.c_uint32, P(ibp_attention), P(ibp_pages)
+        L.ibp_pages_copy.argtypes = [p, p, u64, p, p, p, u64, p, p, u64, p]
+        L.ibp_pages_workspace.argtypes = [u64, u64]
+        L.ibp_pages_alloc.argtypes = [p, p, u64, p, u64, p, u64, p]
+        L.ibp_pages_fork.argtypes = [p, p, u64, p, p, p, u64, u32, u64, p, u32, p, p, u64, p, u64, p]
+        L.ibp_pages_free.argtypes = [p, p, u64, p, u64, u32, u64, p, u64, p]
+        L.ibp_pages_compact.argtypes = [p, p, u64, p, p, p, p, p, u64, p, u64, p]
+        L.ibp_tree_attention_workspace.argtypes = [A]
+        L.ibp_tree_attention.argtypes = [G, G, A, p, p, p, p, p, p, p, p, u32, p, p, p, u64, p]
+        L.ibp_page_bounds.argtypes = [G, u32, u32, p, p, u64, p, p]
+        L.ibp_select_pages_workspace.argtypes = [A]
+        L.ibp_select_pages.argtypes = [p, A, p, p, u64, p, p, p, u32, u32, p, u32, p, u64, p]
+        L.ibp_sparse_attention_workspace.argtypes = [A, u32]
+        L.ibp_sparse_attention.argtypes = [G, G, A, p, p, p, p, p, p, u32, p, p, p, u64, p]
         L.ibp_status_string.argtypes = [st]
         L.ibp_status_string.restype = ctypes.c_char_p
         for f in ABI_FUNCTIONS:
             if f != "ibp_status_string":
-                getattr(L, f).restype = st
+                getattr(L, f).restype = u64 if f.endswith("_workspace") else st
         _lib = L
     return _lib
 
@@ -384,3 +415,266 @@ def ibp_gather_decompress_split(meta: Meta, slots: torch.Tensor, n_slots: int, h
     _check(lib().ibp_gather_decompress_split(meta, _ptr(slots), int(n_slots), _ptr(headers), _ptr(bitmask),
                                              _ptr(ids), int(ids.numel()), _ptr(dst), _stream(stream)),
            "ibp_gather_decompress_split")
+
+
+# ---------------------------------------------------------------------------
+# Pages of a key/value cache: management without decoding, attention that
+# reads them where they lie.  Every call takes an optional torch stream and
+# queues on it (default: torch's current stream of the tensors' device).
+# ---------------------------------------------------------------------------
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+class Pages:
+    """A pool of pages: the slots and bitmask that ibp_compress writes, and
+    the handle of their format.  Keeps the tensors alive; `slots` may be any
+    contiguous tensor of at least n_slots * L bytes, on the GPU or pinned."""
+
+    def __init__(self, meta: Meta, slots: torch.Tensor, n_slots: int, bitmask: torch.Tensor):
+        _need(slots, int(n_slots) * meta.tensor_bytes, "slots")
+        _need(bitmask, _bitmask_bytes(n_slots), "bitmask")
+        self.meta, self.slots, self.n_slots, self.bitmask = meta, slots, int(n_slots), bitmask
+        self.tensor_bytes = meta.tensor_bytes
+        self._struct = ibp_pages(meta.handle, _ptr(slots), self.n_slots, _ptr(bitmask))
+
+    @property
+    def _as_parameter_(self):
+        if not self.meta.handle:
+            raise ValueError("the pool's handle has been closed")
+        return ctypes.byref(self._struct)
+
+
+def _typed(t: torch.Tensor, dtype: torch.dtype, what: str, numel: int | None = None):
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
+    if numel is not None and t.numel() < numel:
+        raise ValueError(f"{what} holds {t.numel()} entries, the call needs {numel}")
+
+
+def _stream_of(stream, t: torch.Tensor) -> ctypes.c_void_p:
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    if _raw_stream is not None and t.is_cuda:
+        return ctypes.c_void_p(_raw_stream(t.device.index))
+    return _stream(None)
+
+
+def _workspace(given: torch.Tensor | None, nbytes: int, like: torch.Tensor, stream):
+    """The caller's workspace, or one of torch's allocator that outlives the
+    call on the stream it is used on."""
+    if given is not None:
+        _need(given, nbytes, "workspace")
+        return given
+    if nbytes == 0:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
+def _bytes_of(t: torch.Tensor | None) -> int:
+    return 0 if t is None else t.nbytes
+
+
+def ibp_pages_copy(meta: Meta, src_slots: torch.Tensor, n_src: int, src_bitmask: torch.Tensor, src_ids: torch.Tensor,
+                   dst_slots: torch.Tensor, n_dst: int, dst_bitmask: torch.Tensor, dst_ids: torch.Tensor,
+                   stream=None):
+    """Item and bit of slot src_ids[i] -> slot dst_ids[i], without decoding
+    (-1 on either side: skipped)."""
+    _typed(src_ids, torch.int64, "src_ids")
+    _typed(dst_ids, torch.int64, "dst_ids", src_ids.numel())
+    L = meta.tensor_bytes
+    _need_all((src_slots, int(n_src) * L, "src_slots"), (dst_slots, int(n_dst) * L, "dst_slots"),
+              (src_bitmask, _bitmask_bytes(n_src), "src_bitmask"), (dst_bitmask, _bitmask_bytes(n_dst), "dst_bitmask"))
+    _check(lib().ibp_pages_copy(meta, _ptr(src_slots), int(n_src), _ptr(src_bitmask), _ptr(src_ids), _ptr(dst_slots),
+                                int(n_dst), _ptr(dst_bitmask), _ptr(dst_ids), src_ids.numel(),
+                                _stream_of(stream, src_ids)), "ibp_pages_copy")
+
+
+def ibp_pages_workspace(n_slots: int, n: int = 0) -> int:
+    return int(lib().ibp_pages_workspace(int(n_slots), int(n)))
+
+
+def ibp_pages_alloc(meta: Meta, refs: torch.Tensor, n_slots: int, ids: torch.Tensor, workspace=None, stream=None):
+    """ids <- the lowest free slots, in order; their counts become 1."""
+    _typed(refs, torch.int32, "refs", int(n_slots))
+    _typed(ids, torch.int64, "ids")
+    ws = _workspace(workspace, ibp_pages_workspace(n_slots), refs, stream)
+    _check(lib().ibp_pages_alloc(meta, _ptr(refs), int(n_slots), _ptr(ids), ids.numel(), _ptr(ws), _bytes_of(ws),
+                                 _stream_of(stream, refs)), "ibp_pages_alloc")
+
+
+def _table_shape(table: torch.Tensor):
+    _typed(table, torch.int64, "table")
+    if table.dim() != 3:
+        raise ValueError("a block table has the shape (sequences, heads, blocks)")
+    return table.shape
+
+
+def ibp_pages_fork(meta: Meta, slots: torch.Tensor, n_slots: int, bitmask: torch.Tensor, refs: torch.Tensor,
+                   table: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor, children: torch.Tensor, *,
+                   page_tokens: int, workspace=None, stream=None):
+    """Sequence children[i] of the table becomes a fork of parents[i]: full
+    pages shared, the partly filled one copied into a free slot."""
+    n_seqs, heads, blocks = _table_shape(table)
+    n = parents.numel()
+    _typed(refs, torch.int32, "refs", int(n_slots))
+    _typed(lens, torch.int32, "lens", n_seqs)
+    _typed(parents, torch.int64, "parents")
+    _typed(children, torch.int64, "children", n)
+    _need_all((slots, int(n_slots) * meta.tensor_bytes, "slots"), (bitmask, _bitmask_bytes(n_slots), "bitmask"))
+    ws = _workspace(workspace, ibp_pages_workspace(n_slots, n * heads), refs, stream)
+    _check(lib().ibp_pages_fork(meta, _ptr(slots), int(n_slots), _ptr(bitmask), _ptr(refs), _ptr(table), n_seqs, heads,
+                                blocks, _ptr(lens), int(page_tokens), _ptr(parents), _ptr(children), n, _ptr(ws),
+                                _bytes_of(ws), _stream_of(stream, refs)), "ibp_pages_fork")
+
+
+def ibp_pages_free(meta: Meta, refs: torch.Tensor, n_slots: int, table: torch.Tensor, seqs: torch.Tensor, stream=None):
+    """Releases every page in the rows `seqs` of the table."""
+    n_seqs, heads, blocks = _table_shape(table)
+    _typed(refs, torch.int32, "refs", int(n_slots))
+    _typed(seqs, torch.int64, "seqs")
+    _check(lib().ibp_pages_free(meta, _ptr(refs), int(n_slots), _ptr(table), n_seqs, heads, blocks, _ptr(seqs),
+                                seqs.numel(), _stream_of(stream, refs)), "ibp_pages_free")
+
+
+def ibp_pages_compact(meta: Meta, slots: torch.Tensor, n_slots: int, bitmask: torch.Tensor, refs: torch.Tensor,
+                      map: torch.Tensor, n_live: torch.Tensor, table: torch.Tensor | None = None, workspace=None,
+                      stream=None):
+    """Live pages moved to slots [0, n_live); map: each slot's new id; the
+    table's ids are rewritten."""
+    _typed(refs, torch.int32, "refs", int(n_slots))
+    _typed(map, torch.int64, "map", int(n_slots))
+    _typed(n_live, torch.int64, "n_live", 1)
+    if table is not None:
+        _typed(table, torch.int64, "table")
+    _need_all((slots, int(n_slots) * meta.tensor_bytes, "slots"), (bitmask, _bitmask_bytes(n_slots), "bitmask"))
+    ws = _workspace(workspace, ibp_pages_workspace(n_slots), refs, stream)
+    _check(lib().ibp_pages_compact(meta, _ptr(slots), int(n_slots), _ptr(bitmask), _ptr(refs), _ptr(map), _ptr(n_live),
+                                   _ptr(table), 0 if table is None else table.numel(), _ptr(ws), _bytes_of(ws),
+                                   _stream_of(stream, refs)), "ibp_pages_compact")
+
+
+def _queries(q: torch.Tensor, table: torch.Tensor, page_tokens: int, scale: float = 1.0) -> ibp_attention:
+    """Shape and strides of the queries (rows, heads, dims), whose dims are
+    contiguous."""
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"q must be bfloat16 or float16, not {q.dtype}")
+    n_seqs, kv_heads, blocks = _table_shape(table)
+    if q.dim() != 3 or (q.shape[2] > 1 and q.stride(2) != 1):
+        raise ValueError("q has the shape (rows, heads, dims) with contiguous dims")
+    return ibp_attention(dtype=_DTYPES[q.dtype], head_dim=q.shape[2], page_tokens=int(page_tokens),
+                         n_q_heads=q.shape[1], n_kv_heads=kv_heads, scale=float(scale), n_rows=q.shape[0],
+                         n_seqs=n_seqs, table_blocks=blocks, q_row_stride=q.stride(0), q_head_stride=q.stride(1))
+
+
+def _outputs(q, out, lse, k: Pages, v: Pages):
+    if out.dtype != q.dtype:
+        raise ValueError(f"out must be {q.dtype}, not {out.dtype}")
+    _need(out, q.numel() * 2, "out")
+    if lse is not None:
+        _typed(lse, torch.float32, "lse", q.shape[0] * q.shape[1])
+    if k.tensor_bytes != v.tensor_bytes:
+        raise ValueError("pages of keys and of values differ in size")
+    row = 2 * q.shape[2]
+    if row == 0 or k.tensor_bytes % row:
+        raise ValueError(f"a page of {k.tensor_bytes} bytes holds no whole rows of {q.shape[2]} numbers")
+    return k.tensor_bytes // row
+
+
+def _dense_ptr(t: torch.Tensor):
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def ibp_tree_attention(k: Pages, v: Pages, q: torch.Tensor, k_table: torch.Tensor, v_table: torch.Tensor,
+                       lens: torch.Tensor, new_rows: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                       mask: torch.Tensor, out: torch.Tensor, lse: torch.Tensor | None = None, *, scale: float,
+                       max_len: int = 0, max_new: int, workspace=None, stream=None):
+    """Attention of drafted tokens (rows new_rows[s] .. new_rows[s + 1] of q,
+    k_new, v_new) over their sequence's pages and over the drafted tokens whose
+    bits their mask row (int64 words) has.  One token per sequence with mask 1
+    is a decoding step."""
+    a = _queries(q, k_table, _outputs(q, out, lse, k, v), scale)
+    if v_table.shape != k_table.shape or v_table.dtype != torch.int64:
+        raise ValueError("the block tables of keys and values differ in shape or type")
+    _typed(lens, torch.int32, "lens", a.n_seqs)
+    _typed(new_rows, torch.int32, "new_rows", a.n_seqs + 1)
+    shape = (q.shape[0], a.n_kv_heads, q.shape[2])
+    for t, what in ((k_new, "k_new"), (v_new, "v_new")):
+        if t.dtype != q.dtype or tuple(t.shape) != shape or (shape[2] > 1 and t.stride(2) != 1):
+            raise ValueError(f"{what} must be {q.dtype} of shape {shape} with contiguous dims")
+    if k_new.stride() != v_new.stride():
+        raise ValueError("k_new and v_new must have the same strides")
+    _typed(mask, torch.int64, "mask")
+    if mask.dim() != 2 or mask.shape[0] < q.shape[0]:
+        raise ValueError("mask has a row of int64 words for each row of q")
+    a.new_row_stride, a.new_head_stride = k_new.stride(0), k_new.stride(1)
+    a.max_len, a.max_new = int(max_len), int(max_new)
+    ref = ctypes.byref(a)
+    ws = _workspace(workspace, int(lib().ibp_tree_attention_workspace(ref)), q, stream)
+    _check(lib().ibp_tree_attention(k, v, ref, _dense_ptr(q), _ptr(k_table), _ptr(v_table), _ptr(lens), _ptr(new_rows),
+                                    _dense_ptr(k_new), _dense_ptr(v_new), _ptr(mask), mask.shape[1], _ptr(out),
+                                    _ptr(lse), _ptr(ws), _bytes_of(ws), _stream_of(stream, q)), "ibp_tree_attention")
+
+
+def ibp_page_bounds(k: Pages, ids: torch.Tensor, tokens: torch.Tensor | None, bounds: torch.Tensor, stream=None):
+    """bounds (n_slots, 2, dims): smallest and largest number of the first
+    tokens[i] tokens of page ids[i]."""
+    _typed(ids, torch.int64, "ids")
+    if bounds.dtype not in _DTYPES or bounds.dim() != 3 or bounds.shape[1] != 2 or bounds.shape[0] < k.n_slots:
+        raise ValueError("bounds must be bfloat16 or float16 of shape (slots, 2, dims)")
+    if tokens is not None:
+        _typed(tokens, torch.int32, "tokens", ids.numel())
+    _check(lib().ibp_page_bounds(k, _DTYPES[bounds.dtype], bounds.shape[2], _ptr(ids), _ptr(tokens), ids.numel(),
+                                 _ptr(bounds), _stream_of(stream, ids)), "ibp_page_bounds")
+
+
+def _rows_of(a: ibp_attention, lens, row_seq):
+    _typed(lens, torch.int32, "lens", a.n_rows)
+    if row_seq is not None:
+        _typed(row_seq, torch.int32, "row_seq", a.n_rows)
+    elif a.n_rows > a.n_seqs:
+        raise ValueError("more rows than sequences need row_seq")
+
+
+def _block_lists(a: ibp_attention, blocks: torch.Tensor) -> int:
+    _typed(blocks, torch.int32, "blocks")
+    if blocks.dim() != 3 or blocks.shape[0] != a.n_rows or blocks.shape[1] != a.n_kv_heads:
+        raise ValueError("blocks has the shape (rows, key/value heads, blocks)")
+    return blocks.shape[2]
+
+
+def ibp_select_pages(q: torch.Tensor, bounds: torch.Tensor, k_table: torch.Tensor, lens: torch.Tensor,
+                     blocks: torch.Tensor, *, meta: Meta, page_tokens: int, keep_first: int = 0, keep_last: int = 0,
+                     row_seq: torch.Tensor | None = None, workspace=None, stream=None):
+    """blocks (rows, key/value heads, n) <- the block numbers that each query
+    reads: the first and last ones kept, and those with the highest bound on
+    the score; ascending, -1 behind."""
+    a = _queries(q, k_table, page_tokens)
+    if bounds.dtype != q.dtype or bounds.dim() != 3 or bounds.shape[1] != 2 or bounds.shape[2] != q.shape[2]:
+        raise ValueError("bounds must be of q's type and of shape (slots, 2, dims)")
+    _rows_of(a, lens, row_seq)
+    n = _block_lists(a, blocks)
+    ref = ctypes.byref(a)
+    ws = _workspace(workspace, int(lib().ibp_select_pages_workspace(ref)), q, stream)
+    _check(lib().ibp_select_pages(meta, ref, _dense_ptr(q), _ptr(bounds), bounds.shape[0], _ptr(k_table), _ptr(lens),
+                                  _ptr(row_seq), int(keep_first), int(keep_last), _ptr(blocks), n, _ptr(ws),
+                                  _bytes_of(ws), _stream_of(stream, q)), "ibp_select_pages")
+
+
+def ibp_sparse_attention(k: Pages, v: Pages, q: torch.Tensor, k_table: torch.Tensor, v_table: torch.Tensor,
+                         lens: torch.Tensor, blocks: torch.Tensor, out: torch.Tensor,
+                         lse: torch.Tensor | None = None, *, scale: float, row_seq: torch.Tensor | None = None,
+                         workspace=None, stream=None):
+    """Attention of each row over the pages that `blocks` lists for it."""
+    a = _queries(q, k_table, _outputs(q, out, lse, k, v), scale)
+    if v_table.shape != k_table.shape or v_table.dtype != torch.int64:
+        raise ValueError("the block tables of keys and values differ in shape or type")
+    _rows_of(a, lens, row_seq)
+    n = _block_lists(a, blocks)
+    ref = ctypes.byref(a)
+    ws = _workspace(workspace, int(lib().ibp_sparse_attention_workspace(ref, n)), q, stream)
+    _check(lib().ibp_sparse_attention(k, v, ref, _dense_ptr(q), _ptr(k_table), _ptr(v_table), _ptr(lens),
+                                      _ptr(row_seq), _ptr(blocks), n, _ptr(out), _ptr(lse), _ptr(ws), _bytes_of(ws),
+                                      _stream_of(stream, q)), "ibp_sparse_attention")
