@@ -269,7 +269,7 @@ ibp_status ibp_gather_decompress_split(ibp_meta_t meta, const void* slots, uint6
  * bytes, 16-byte aligned slots and at most 2^32 - 2 of them; otherwise they
  * return IBP_ERR_UNSUPPORTED or IBP_ERR_INVALID_ARG.  None allocates memory
  * or reads results on the host, so every one may be captured in a HIP graph;
- * scratch comes from the caller (`workspace`, device, 8-byte aligned), and
+ * scratch comes from the caller (`workspace`, device, 16-byte aligned), and
  * two calls that may overlap in time must not share it.  Ids that are neither
  * -1 nor a slot latch IBP_ERR_RANGE.
  * ------------------------------------------------------------------------- */

@@ -460,7 +460,7 @@ uint64_t ibp_pages_workspace(uint64_t n_slots, uint64_t n) {
 }
 
 static ibp_status check_workspace(ibp_meta_t h, const void* ws, uint64_t bytes, uint64_t need) {
-    if (bytes < need || !device_only(ws, h->device) || reinterpret_cast<uintptr_t>(ws) % 8) return IBP_ERR_INVALID_ARG;
+    if (bytes < need || !device_only(ws, h->device) || reinterpret_cast<uintptr_t>(ws) % 16) return IBP_ERR_INVALID_ARG;
     return IBP_OK;
 }
 

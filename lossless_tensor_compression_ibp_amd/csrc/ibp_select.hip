@@ -8,9 +8,8 @@
 // rounds once; the kernels get there in two steps:
 //   1. k_scores multiplies on the matrix cores in 32 bits, and a second
 //      product of the absolute values bounds how far each sum can be off;
-//   2. k_choose finds the n-th largest of these, and sums again in 64 bits
-//      only the pages whose distance from it is within that bound, usually
-//      none or one.
+//   2. k_choose finds the n-th largest of these, roughly, and sums again in 64
+//      bits only the pages that lie within that bound of it, usually a few.
 // The result is the one that 64-bit sums of all pages give.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -105,11 +104,19 @@ __global__ __launch_bounds__(kWave * kBoundWaves) void k_page_bounds(Pool pool, 
 }
 
 // ---------------------------------------------------------------------------
-// Scores.  One wave takes 16 * kPageTiles blocks of one (row tile, head): the
-// bounds of 16 pages are the A operand (lane l: page l % 16, eight dims), 16
-// columns of (row, query head) the B operand, so D holds the scores of 16
-// pages by 16 columns.  A row tile is 16 / group rows (one, and several column
-// tiles, for groups of more than 16 heads).
+// Scores.  A operand: 16 columns of (row, query head), lane l holding column
+// l % 16; B operand: the bounds of 16 pages.  D then holds, in lane l, page
+// l % 16 and columns 4 (l / 16) .. + 3, so the maximum over a group's heads is
+// taken inside a lane for groups of up to four heads and across the four
+// lanes of a page for larger ones.  Groups are padded to `pad` heads (1, 2, 4,
+// 8 or a multiple of 16), so that no group straddles tiles.
+//
+// A wave takes 64 blocks of one head for CT tiles of columns, the next 16
+// pages' bounds in flight while it multiplies.  Decoding, where every row has
+// pages of its own, takes CT = 1 and other blocks in every wave, and is bound
+// by the bounds' bytes.  Where rows share a sequence the four waves of a
+// workgroup take the same blocks for different rows, so that three of them
+// find the bounds in the compute unit's cache.
 // ---------------------------------------------------------------------------
 struct SelectArgs {
     const void* q;
@@ -117,380 +124,582 @@ struct SelectArgs {
     const int64_t* table;
     const int32_t* lens;
     const int32_t* row_seq;
-    float* scores;   // [n_rows][kv heads][blocks]
-    float* slack;    // [n_rows][kv heads][chunks]: bound on the error of a chunk's scores
+    float* scores;   // [n_rows][kv heads][pitch]
+    float* slack;    // [n_rows][kv heads][chunks]: sum of absolute products, the largest of 64 blocks
     int32_t* out;
     uint32_t* err;
-    uint64_t n_rows, n_seqs, n_slots, blocks, chunks;
+    uint64_t n_rows, n_seqs, n_slots, blocks, pitch, chunks;
     int64_t q_row, q_head;
     uint32_t kv_heads, group, page_tokens, keep_first, keep_last, n_out;
-    uint32_t rows_per_tile, col_tiles;
-    uint32_t vec;    // q rows may be read as 16-byte vectors
+    uint32_t pad;            // heads a group takes in a tile's columns
+    uint32_t log2_pad;       // its logarithm, 31 for groups of several tiles
+    uint32_t rows_per_tile;  // 16 / pad, or 1
+    uint32_t head_tiles;     // column tiles of one row (pad / 16, or 1)
+    uint32_t wave_rows;      // rows of one wave
+    uint32_t span;           // times 64 blocks per wave
+    uint32_t same_blocks;    // a workgroup's waves take the same blocks, and rows of their own
+    uint32_t vec;            // q rows may be read as 16-byte vectors
 };
 
 constexpr uint32_t kScoreWaves = 4;
-constexpr uint32_t kPageTiles = 4;  // tiles of 16 blocks per wave
-constexpr uint32_t kScoreChunk = kScoreWaves * kPageTiles * 16;
+constexpr uint32_t kWaveBlocks = 64;
 
 // Error of a 32-bit sum of 2 * head_dim products, relative to the sum of
 // their absolute values: head_dim <= 256, so at most 512 additions of 2^-24
 // each, 2^-15; the products themselves are exact.
 constexpr float kSumError = 1.0f / 32768.0f;
 
-// Blocks of row r, and whether its sequence and length are valid.
-__device__ __forceinline__ uint64_t row_blocks(const SelectArgs& a, uint64_t r, int64_t* seq) {
-    *seq = a.row_seq ? a.row_seq[r] : (int64_t)r;
+// Blocks of row r (0 where its sequence or length is not valid).
+__device__ __forceinline__ uint32_t row_blocks(const SelectArgs& a, uint64_t r, int64_t* seq) {
+    *seq = a.row_seq ? (int64_t)a.row_seq[r] : (int64_t)r;
     const int64_t len = a.lens[r];
     if (*seq < 0 || (uint64_t)*seq >= a.n_seqs || len < 0) return 0;
     const uint64_t nb = ((uint64_t)len + a.page_tokens - 1) / a.page_tokens;
-    return nb < a.blocks ? nb : a.blocks;
+    return (uint32_t)(nb < a.blocks ? nb : a.blocks);
 }
 
-template <class E, int D>
-__global__ __launch_bounds__(kWave * kScoreWaves) void k_scores(SelectArgs a) {
+template <class E, int D, int CT>
+__global__ __launch_bounds__(kWave * kScoreWaves, 2) void k_scores(SelectArgs a) {
     using V8 = typename E::V8;
+    constexpr int DK = D / 32;
     const uint32_t lane = lane_id(), wib = uniform(threadIdx.x / kWave);
     const uint32_t col = lane & 15u, g = lane >> 4;
     const uint32_t h = blockIdx.y;
-    const uint64_t r0 = (uint64_t)blockIdx.z * a.rows_per_tile;
-    const uint64_t b0 = (uint64_t)blockIdx.x * kScoreChunk + wib * (kPageTiles * 16);
-    // the tile's rows that have not been done yet, one sequence after another
-    int64_t row_seq = -1;
-    uint64_t row_nb = 0;
-    if (lane < a.rows_per_tile && r0 + lane < a.n_rows) row_nb = row_blocks(a, r0 + lane, &row_seq);
-    uint64_t todo = ballot(row_nb > b0);
-    const bool one_tile = a.col_tiles == 1;
-    while (todo) {
+    const uint64_t r0 = ((uint64_t)blockIdx.z * (a.same_blocks ? kScoreWaves : 1u) + (a.same_blocks ? wib : 0u)) * a.wave_rows;
+    const uint32_t b_first = (a.same_blocks ? blockIdx.x : blockIdx.x * kScoreWaves + wib) * kWaveBlocks * a.span;
+    // lane l: row r0 + l of the wave (at most 64), its sequence and blocks
+    int64_t my_seq = -1;
+    uint32_t my_nb = 0;
+    if (lane < a.wave_rows && r0 + lane < a.n_rows) my_nb = row_blocks(a, r0 + lane, &my_seq);
+    uint64_t todo = ballot(my_nb > b_first);
+    while (todo) {  // one sequence after another; usually there is one
         const uint32_t lead = (uint32_t)__builtin_ctzll(todo);
-        const int64_t seq = (int64_t)(((uint64_t)lane_value((uint32_t)((uint64_t)row_seq >> 32), lead) << 32) |
-                                      lane_value((uint32_t)row_seq, lead));
-        const uint64_t mine = todo & ballot(row_seq == seq && row_nb > b0);
+        const uint32_t seq = lane_value((uint32_t)my_seq, (int)lead);
+        const uint64_t mine = todo & ballot((uint32_t)my_seq == seq && my_nb > b_first);
         todo &= ~mine;
-        uint64_t nb = 0;
-        for (uint64_t m = mine; m; m &= m - 1) {
-            const uint32_t l = (uint32_t)__builtin_ctzll(m);
-            nb = max(nb, (uint64_t)lane_value((uint32_t)row_nb, l));
-        }
-        const int64_t* table = a.table + ((uint64_t)seq * a.kv_heads + h) * a.blocks;
-        for (uint32_t t = 0; t < kPageTiles; ++t) {
-            const uint64_t bt = b0 + 16 * t;
-            if (bt >= nb) break;
-            const uint64_t bl = bt + col;
-            uint32_t id = kNoPage;
-            if (bl < nb) {
-                id = page_id(table[bl], (uint32_t)a.n_slots);
-                if (id == kNoPage) atomicCAS(a.err, 0u, (uint32_t)kErrRange);
-            }
-            const char* base = static_cast<const char*>(a.bounds) + (uint64_t)(id == kNoPage ? 0u : id) * (4ull * D);
-            V8 lo[D / 32], hi[D / 32];
+        uint32_t nb = 0;
+        for (uint64_t m = mine; m; m &= m - 1) nb = max(nb, lane_value(my_nb, (int)__builtin_ctzll(m)));
+        // 64 page ids at once
+        auto ids_at = [&](uint32_t b) __attribute__((always_inline)) -> uint32_t {
+            if (b + lane >= nb) return kNoPage;
+            const uint32_t id =
+                page_id(a.table[((uint64_t)seq * a.kv_heads + h) * a.blocks + b + lane], (uint32_t)a.n_slots);
+            if (id == kNoPage) atomicCAS(a.err, 0u, (uint32_t)kErrRange);
+            return id;
+        };
+        const uint32_t b_end = min(nb, b_first + kWaveBlocks * a.span);
+        const uint32_t col_tiles = a.head_tiles * ((a.wave_rows + a.rows_per_tile - 1) / a.rows_per_tile);
+        for (uint32_t ct0 = 0; ct0 < col_tiles; ct0 += CT) {
+            // the numbers above zero, and those below, of each column
+            V8 qp[CT][DK], qm[CT][DK];
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) {
-                lo[kk] = *reinterpret_cast<const V8*>(base + 64 * kk + 16 * g);
-                hi[kk] = *reinterpret_cast<const V8*>(base + 2 * D + 64 * kk + 16 * g);
-            }
-            float best[4], off[4];
+            for (int c = 0; c < CT; ++c) {
+                const uint32_t x = (ct0 + c) * 16 + col;  // column of the wave
+                const uint32_t row = x >> a.log2_pad, head = x - (row << a.log2_pad);
+                const bool on = head < a.group && row < a.wave_rows && ((mine >> (row & 63u)) & 1u);
+                const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)(r0 + row) * a.q_row +
+                                    (int64_t)(h * a.group + head) * a.q_head;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                best[i] = -__builtin_inff();
-                off[i] = 0.f;
-            }
-            for (uint32_t ct = 0; ct < a.col_tiles; ++ct) {
-                // column -> (row of the tile, query head of the group)
-                const uint32_t c = ct * 16 + col;
-                const uint32_t row = one_tile ? c / a.group : 0u, head = one_tile ? c - row * a.group : c;
-                const bool on = head < a.group && row < a.rows_per_tile && r0 + row < a.n_rows;
-                f32x4 s = {0.f, 0.f, 0.f, 0.f}, w = {0.f, 0.f, 0.f, 0.f};
-                const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (int64_t)(r0 + row) * a.q_row +
-                                     (int64_t)(h * a.group + head) * a.q_head;
-#pragma unroll
-                for (int kk = 0; kk < D / 32; ++kk) {
-                    const u32x4 x = on ? load_eight(qp + 32 * kk + 8 * g, a.vec != 0) : u32x4{0u, 0u, 0u, 0u};
-                    u32x4 p, m, pa, ma;
+                for (int kk = 0; kk < DK; ++kk) {
+                    const u32x4 v = on ? load_eight(q + 32 * kk + 8 * g, a.vec != 0) : u32x4{0u, 0u, 0u, 0u};
+                    u32x4 p, m;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        // the numbers above zero, and those below, of two at a time
-                        const uint32_t neg = (x[j] >> 15 & 0x10001u) * 0xFFFFu;
-                        p[j] = x[j] & ~neg;
-                        m[j] = x[j] & neg;
-                        pa[j] = p[j] & 0x7FFF7FFFu;
-                        ma[j] = m[j] & 0x7FFF7FFFu;
+                        const uint32_t neg = (v[j] >> 15 & 0x10001u) * 0xFFFFu;
+                        p[j] = v[j] & ~neg;
+                        m[j] = v[j] & neg;
                     }
-                    s = E::mfma(hi[kk], bits_as<V8>(p), s);
-                    s = E::mfma(lo[kk], bits_as<V8>(m), s);
-                    w = E::mfma(bits_as<V8>(bits_as<u32x4>(hi[kk]) & 0x7FFF7FFFu), bits_as<V8>(pa), w);
-                    w = E::mfma(bits_as<V8>(bits_as<u32x4>(lo[kk]) & 0x7FFF7FFFu), bits_as<V8>(ma), w);
+                    qp[c][kk] = bits_as<V8>(p);
+                    qm[c][kk] = bits_as<V8>(m);
                 }
+            }
+            // of columns 4 g + i of each tile: which hold a head, the row of
+            // the first, and the blocks of each row they belong to
+            uint32_t heads[CT], row_nb[CT][4];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                heads[c] = 0;
+                const uint32_t x0 = (ct0 + c) * 16 + 4 * g;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (!on) s[i] = -__builtin_inff();
-                    if (!on || !(w[i] < __builtin_inff())) w[i] = 0.f;
-                    best[i] = fmaxf(best[i], s[i]);  // a NaN is left out
-                    off[i] = fmaxf(off[i], w[i]);
+                    const uint32_t row = (x0 + i) >> a.log2_pad;
+                    if (x0 + i - (row << a.log2_pad) < a.group) heads[c] |= 1u << i;
+                    const bool live = row < a.wave_rows && ((mine >> (row & 63u)) & 1u);
+                    const uint32_t n = (uint32_t)__shfl((int)my_nb, (int)(row & 63u));
+                    row_nb[c][i] = live ? n : 0u;
                 }
             }
-            // the highest over a row's heads: its columns, or (one row) all 16
-            float slack = 0.f;
+            uint32_t id_next = ids_at(b_first);
+            for (uint32_t b0 = b_first; b0 < b_end; b0 += kWaveBlocks) {
+                const uint32_t id = id_next;
+                id_next = b0 + kWaveBlocks < b_end ? ids_at(b0 + kWaveBlocks) : kNoPage;
+                const uint32_t tiles = min((b_end - b0 + 15) / 16, kWaveBlocks / 16);
+                V8 lo[DK], hi[DK], lo_next[DK], hi_next[DK];
+                auto fetch = [&](uint32_t t) __attribute__((always_inline)) {
+                    const uint32_t pid = (uint32_t)__shfl((int)id, (int)(16 * t + col));
+                    const char* base =
+                        static_cast<const char*>(a.bounds) + (uint64_t)(pid == kNoPage ? 0u : pid) * (4ull * D) + 16 * g;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v = best[i], e = off[i];
-                if (one_tile) {
-                    for (uint32_t k = 1; k < a.group; ++k) {
-                        v = fmaxf(v, __shfl(best[i], (int)(lane + k) & 63));
-                        e = fmaxf(e, __shfl(off[i], (int)(lane + k) & 63));
+                    for (int kk = 0; kk < DK; ++kk) {
+                        lo_next[kk] = *reinterpret_cast<const V8*>(base + 64 * kk);
+                        hi_next[kk] = *reinterpret_cast<const V8*>(base + 2 * D + 64 * kk);
                     }
-                } else {
-                    for (int o = 1; o < 16; o <<= 1) {
-                        v = fmaxf(v, __shfl_xor(v, o));
-                        e = fmaxf(e, __shfl_xor(e, o));
+                };
+                fetch(0);
+                float slack[CT];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) slack[c] = 0.f;
+                for (uint32_t t = 0; t < tiles; ++t) {
+#pragma unroll
+                    for (int kk = 0; kk < DK; ++kk) {
+                        lo[kk] = lo_next[kk];
+                        hi[kk] = hi_next[kk];
+                    }
+                    if (t + 1 < tiles) fetch(t + 1);
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) {
+                        f32x4 s = {0.f, 0.f, 0.f, 0.f}, wp = s, wm = s;
+#pragma unroll
+                        for (int kk = 0; kk < DK; ++kk) {
+                            s = E::mfma(qp[c][kk], hi[kk], s);
+                            s = E::mfma(qm[c][kk], lo[kk], s);
+                            wp = E::mfma(qp[c][kk], bits_as<V8>(bits_as<u32x4>(hi[kk]) & 0x7FFF7FFFu), wp);
+                            wm = E::mfma(qm[c][kk], bits_as<V8>(bits_as<u32x4>(lo[kk]) & 0x7FFF7FFFu), wm);
+                        }
+                        const uint32_t x0 = (ct0 + c) * 16 + 4 * g, row0 = x0 >> a.log2_pad;
+                        const uint32_t b = b0 + 16 * t + col;
+                        float v[4], w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            // a NaN is left out: fmaxf takes its other argument
+                            v[i] = (heads[c] >> i) & 1u ? fmaxf(s[i], -__builtin_inff()) : -__builtin_inff();
+                            w[i] = wp[i] - wm[i];
+                            w[i] = w[i] < __builtin_inff() ? w[i] : 0.f;
+                        }
+                        if (a.pad >= 4) {
+                            float m = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+                            float e = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+                            if (a.pad >= 8) {
+                                m = fmaxf(m, __shfl_xor(m, 16));
+                                e = fmaxf(e, __shfl_xor(e, 16));
+                            }
+                            if (a.pad >= 16) {
+                                m = fmaxf(m, __shfl_xor(m, 32));
+                                e = fmaxf(e, __shfl_xor(e, 32));
+                            }
+                            if (b < row_nb[c][0]) {
+                                slack[c] = fmaxf(slack[c], e);
+                                const bool later = a.head_tiles > 1 && ct0 + c > 0;
+                                if (x0 == (row0 << a.log2_pad) || (later && g == 0)) {
+                                    float* to = a.scores + ((r0 + row0) * a.kv_heads + h) * a.pitch + b;
+                                    if (later) m = fmaxf(m, *to);  // a row of several tiles: the highest so far
+                                    *to = m;
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (a.pad == 2 && (i & 1)) continue;
+                                const float m = a.pad == 2 ? fmaxf(v[i], v[i | 1]) : v[i];
+                                const float e = a.pad == 2 ? fmaxf(w[i], w[i | 1]) : w[i];
+                                if (b < row_nb[c][i]) {
+                                    slack[c] = fmaxf(slack[c], e);
+                                    a.scores[((r0 + ((x0 + i) >> a.log2_pad)) * a.kv_heads + h) * a.pitch + b] = m;
+                                }
+                            }
+                        }
                     }
                 }
-                const uint32_t row = one_tile ? col / a.group : 0u;
-                const bool lead_col = one_tile ? col == row * a.group : col == 0;
-                const uint64_t b = bt + 4 * g + i;
-                const bool live = lead_col && row < a.rows_per_tile && ((mine >> row) & 1u) != 0;
-                const uint64_t nb_row = (uint64_t)__shfl((int)(uint32_t)row_nb, (int)min(row, 63u));
-                if (live && b < nb_row) {
-                    a.scores[((r0 + row) * a.kv_heads + h) * a.blocks + b] = v;
-                    slack = fmaxf(slack, e);
+                // The largest sum of the 64 blocks for the rows of lane l's
+                // columns.  Rows that share a lane share the larger one: a bound
+                // may be too large.
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    float e = slack[c];
+                    for (int o = 1; o < 16; o <<= 1) e = fmaxf(e, __shfl_xor(e, o));
+                    const uint32_t x0 = (ct0 + c) * 16 + 4 * g;
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i) {
+                        const uint32_t row = (x0 + i) >> a.log2_pad;
+                        const bool first = a.head_tiles > 1 ? g == 0 && i == 0 : x0 + i == (row << a.log2_pad);
+                        if (col == 0 && first && row_nb[c][i] > b0) {
+                            float* to = a.slack + ((r0 + row) * a.kv_heads + h) * a.chunks + b0 / kWaveBlocks;
+                            if (a.head_tiles > 1 && ct0 + c > 0) e = fmaxf(e, *to);
+                            *to = e;
+                        }
+                    }
                 }
             }
-            // the largest error bound of these 16 blocks, per row
-            slack = fmaxf(slack, __shfl_xor(slack, 16));
-            slack = fmaxf(slack, __shfl_xor(slack, 32));
-            const uint32_t row = one_tile ? col / a.group : 0u;
-            const bool lead_col = one_tile ? col == row * a.group : col == 0;
-            if (g == 0 && lead_col && row < a.rows_per_tile && ((mine >> row) & 1u))
-                a.slack[((r0 + row) * a.kv_heads + h) * a.chunks + bt / 16] = slack * kSumError;
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// The choice.  One workgroup per (row, head).
+// The choice.  One workgroup per (row, head).  A thread has consecutive
+// blocks, whose keys (scores as ordered integers) lie in LDS, or for rows too
+// long for that are made anew from the scores in each pass.  The loops are
+// kept rolled: unrolled over keys in registers the kernel took twice as long
+// on a short row, most of it instruction fetches.
 // ---------------------------------------------------------------------------
-constexpr uint32_t kChooseThreads = 512;
-constexpr uint32_t kChooseWaves = kChooseThreads / kWave;
+constexpr uint64_t kLdsKeys = 8192;
 constexpr uint64_t kMaxBlocks = 1u << 17;  // near blocks are marked in 16 KiB of LDS
 
 // Ascending order as unsigned numbers; NaN the lowest.
 __device__ __forceinline__ uint32_t order_of(float x) {
-    const uint32_t u = __float_as_uint(x);
-    if (x != x) return 0u;
-    const uint32_t k = (u >> 31) ? ~u : u | 0x80000000u;
-    return x == 0.f ? 0x80000000u : k;  // both zeros are one value
+    const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);  // both zeros are one value
+    const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    return x != x ? 0u : k;
 }
 
 __device__ __forceinline__ float value_of(uint32_t k) {
     return __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k);
 }
 
+constexpr uint32_t kMaxChooseWaves = 16;
+constexpr uint32_t kBins = 2048;
+constexpr uint32_t kNearList = kWave;  // near blocks that one wave ranks
+
 struct ChooseShared {
-    uint32_t hist[256];
-    uint32_t sums[kChooseWaves];
-    float slack[kChooseWaves];
-    uint32_t digit, left, in_count;
+    uint32_t hist[kBins];
+    uint32_t sums[2][2][kMaxChooseWaves];
+    uint32_t digit, left, n_near;
+    uint32_t near_block[kNearList], near_key[kNearList];
 };
 
-__device__ __forceinline__ uint32_t choose_sum(uint32_t v, ChooseShared& sh) {
-    v = wave_sum(v);
+// Sums of two numbers over the workgroup, and over the threads in front.
+// `turn` alternates between two rows of LDS, so one barrier per call is
+// enough.
+struct Sums {
+    uint32_t all[2], before[2];
+};
+__device__ __forceinline__ Sums choose_sums(uint32_t v0, uint32_t v1, ChooseShared& sh, uint32_t& turn) {
+    const uint32_t w = threadIdx.x / kWave, waves = blockDim.x / kWave;
+    const uint32_t i0 = wave_incl_scan(v0), i1 = wave_incl_scan(v1);
+    if (lane_id() == kWave - 1) {
+        sh.sums[turn][0][w] = i0;
+        sh.sums[turn][1][w] = i1;
+    }
     __syncthreads();
-    if (lane_id() == 0) sh.sums[threadIdx.x / kWave] = v;
-    __syncthreads();
-    uint32_t s = 0;
-    for (uint32_t i = 0; i < kChooseWaves; ++i) s += sh.sums[i];
+    Sums s{{0, 0}, {i0 - v0, i1 - v1}};
+    for (uint32_t i = 0; i < waves; ++i) {
+        const uint32_t x = sh.sums[turn][0][i], y = sh.sums[turn][1][i];
+        if (i < w) {
+            s.before[0] += x;
+            s.before[1] += y;
+        }
+        s.all[0] += x;
+        s.all[1] += y;
+    }
+    turn ^= 1;
     return s;
 }
 
-// The want-th largest (want >= 1) of key(b) over the blocks b in [0, nb) for
-// which on(b); *above: how many are larger.  Four passes of eight bits.
-template <class On, class Key>
-__device__ __forceinline__ uint32_t nth_largest(uint64_t nb, uint32_t want, ChooseShared& sh, uint32_t* above, On on,
-                                                Key key) {
-    uint32_t prefix = 0, left = want;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (uint32_t i = threadIdx.x; i < 256; i += kChooseThreads) sh.hist[i] = 0;
-        __syncthreads();
-        for (uint64_t b = threadIdx.x; b < nb; b += kChooseThreads) {
-            if (!on(b)) continue;
-            const uint32_t k = key(b);
-            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-                atomicAdd(&sh.hist[(k >> shift) & 255u], 1u);
-        }
-        __syncthreads();
-        if (threadIdx.x < kWave) {
-            // lane l: digits 255 - 4 l .. 252 - 4 l, from the largest
-            const uint32_t lane = lane_id();
-            uint32_t c[4], tot = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                c[j] = sh.hist[255 - 4 * lane - j];
-                tot += c[j];
-            }
-            const uint32_t incl = wave_incl_scan(tot);
-            uint32_t before = incl - tot;
-            const uint64_t has = ballot(incl >= left);
-            if (has && lane == (uint32_t)__builtin_ctzll(has)) {
-                uint32_t j = 0;
-                while (j < 3 && before + c[j] < left) before += c[j++];
-                sh.digit = 255 - 4 * lane - j;
-                sh.left = left - before;
-            }
-        }
-        __syncthreads();
-        prefix |= sh.digit << shift;
-        left = sh.left;
-        __syncthreads();
+// Maxima of two numbers over the workgroup.
+__device__ __forceinline__ void choose_max2(uint32_t& v0, uint32_t& v1, ChooseShared& sh, uint32_t& turn) {
+    for (int o = 32; o > 0; o >>= 1) {
+        v0 = max(v0, (uint32_t)__shfl_xor((int)v0, o));
+        v1 = max(v1, (uint32_t)__shfl_xor((int)v1, o));
     }
-    *above = want - left;
-    return prefix;
+    if (lane_id() == 0) {
+        sh.sums[turn][0][threadIdx.x / kWave] = v0;
+        sh.sums[turn][1][threadIdx.x / kWave] = v1;
+    }
+    __syncthreads();
+    for (uint32_t i = 0; i < blockDim.x / kWave; ++i) {
+        v0 = max(v0, sh.sums[turn][0][i]);
+        v1 = max(v1, sh.sums[turn][1][i]);
+    }
+    turn ^= 1;
 }
 
+// One pass over the bins that each() calls back with: the bin of the left-th
+// largest; `left` becomes its rank within the bin.
+template <class Each>
+__device__ __forceinline__ uint32_t find_bin(uint32_t n_bins, uint32_t& left, ChooseShared& sh, uint32_t& turn,
+                                             Each each) {
+    for (uint32_t i = threadIdx.x; i < n_bins; i += blockDim.x) sh.hist[i] = 0;
+    __syncthreads();
+    each([&](uint32_t bin) __attribute__((always_inline)) { atomicAdd(&sh.hist[bin], 1u); });
+    __syncthreads();
+    // thread t: `per` bins from the top downwards
+    const uint32_t per = (n_bins + blockDim.x - 1) / blockDim.x;
+    const uint32_t top = n_bins - 1 - min(threadIdx.x * per, n_bins - 1);
+    const uint32_t mine = threadIdx.x * per < n_bins ? min(per, n_bins - threadIdx.x * per) : 0u;
+    uint32_t sum = 0;
+    for (uint32_t j = 0; j < mine; ++j) sum += sh.hist[top - j];
+    const Sums s = choose_sums(sum, 0u, sh, turn);
+    uint32_t before = s.before[0];
+    if (before < left && before + sum >= left) {
+        uint32_t j = 0;
+        while (before + sh.hist[top - j] < left) before += sh.hist[top - j++];
+        sh.digit = top - j;
+        sh.left = left - before;
+    }
+    __syncthreads();
+    left = sh.left;
+    return sh.digit;
+}
+
+// The want-th largest (want >= 1) of the keys for which each() calls back;
+// *above: how many are larger.  lo, hi: the smallest and the largest of them.
+template <class Each>
+__device__ __forceinline__ uint32_t nth_largest(uint32_t want, uint32_t lo, uint32_t hi, ChooseShared& sh,
+                                                uint32_t& turn, uint32_t* above, Each each) {
+    *above = 0;
+    if (lo == hi) return lo;
+    const uint32_t lz = (uint32_t)__builtin_clz(hi - lo);
+    uint32_t prefix = 0, left = want;
+    for (int shift = 24; shift > -8; shift -= 8) {
+        if (shift + 8 <= (int)lz) break;  // the bits below are zeros of the shift
+        const uint32_t digit = find_bin(256, left, sh, turn, [&](auto f) __attribute__((always_inline)) {
+            each([&](uint32_t key) __attribute__((always_inline)) {
+                const uint32_t k = (key - lo) << lz;
+                if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) f((k >> shift) & 255u);
+            });
+        });
+        prefix |= digit << shift;
+    }
+    *above = want - left;
+    return lo + (prefix >> lz);
+}
+
+// One wave: the score of page b of (row r, head h) summed in 64 bits, as a
+// key.  Sixteen lanes take a query head, eight dims each at a time.
 template <class E, int D>
-__global__ __launch_bounds__(kChooseThreads) void k_choose(SelectArgs a) {
+__device__ __forceinline__ uint32_t exact_key(const SelectArgs& a, uint64_t r, uint32_t h, const uint16_t* bounds) {
+    const uint32_t lane = lane_id(), part = lane & 15u;
+    float best = -__builtin_inff();
+    for (uint32_t j0 = 0; j0 < a.group; j0 += 4) {
+        const uint32_t j = j0 + (lane >> 4);
+        const uint16_t* q =
+            static_cast<const uint16_t*>(a.q) + (int64_t)r * a.q_row + (int64_t)(h * a.group + min(j, a.group - 1)) * a.q_head;
+        double s = 0.0;
+#pragma unroll
+        for (int d = 0; d < D; d += 128) {
+            if (d + 8 * part < (uint32_t)D) {
+                const u32x4 x = load_eight(q + d + 8 * part, a.vec != 0);
+                const u32x4 lo = *reinterpret_cast<const u32x4*>(bounds + d + 8 * part);
+                const u32x4 hi = *reinterpret_cast<const u32x4*>(bounds + D + d + 8 * part);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int sh = 16 * (e & 1);
+                    const double y = (double)E::from_bits(x[e >> 1] >> sh);
+                    s += (y > 0.0 ? y : 0.0) * (double)E::from_bits(hi[e >> 1] >> sh) +
+                         (y < 0.0 ? y : 0.0) * (double)E::from_bits(lo[e >> 1] >> sh);
+                }
+            }
+        }
+        for (int o = 8; o > 0; o >>= 1) s += __shfl_xor(s, o);
+        best = fmaxf(best, (float)s);  // a head listed twice at the end changes no maximum
+    }
+    best = fmaxf(best, __shfl_xor(best, 16));
+    best = fmaxf(best, __shfl_xor(best, 32));
+    return order_of(best);
+}
+
+template <class E, int D, bool KEYS>
+__global__ __launch_bounds__(1024) void k_choose(SelectArgs a) {
     __shared__ ChooseShared sh;
-    extern __shared__ uint32_t near_bits[];  // blocks to be summed in 64 bits
+    extern __shared__ uint32_t smem[];
+    uint32_t* const near_words = smem;  // blocks to be summed in 64 bits
+    uint32_t* const keys = smem + (a.blocks + 31) / 32;
     const uint64_t rh = blockIdx.x;
     const uint64_t r = rh / a.kv_heads;
     const uint32_t h = (uint32_t)(rh % a.kv_heads);
-    const uint32_t tid = threadIdx.x, lane = lane_id(), wib = tid / kWave;
+    const uint32_t tid = threadIdx.x, nt = blockDim.x, lane = lane_id(), wib = tid / kWave;
     int32_t* out = a.out + rh * a.n_out;
+    float* scores = a.scores + rh * a.pitch;
+    // the first scores and bounds are on their way while the row's length is
+    // (their addresses lie inside the workspace whatever it is)
+    float first = 0.f, slack = 0.f;
+    if (KEYS && tid < a.blocks) first = scores[tid];
+    for (uint32_t c = tid; c < a.chunks; c += nt) slack = a.slack[rh * a.chunks + c];
     int64_t seq;
-    const uint64_t nb = row_blocks(a, r, &seq);
+    const uint32_t nb = row_blocks(a, r, &seq);
     if (tid == 0) {
         const int64_t len = a.lens[r];
         if (seq < 0 || (uint64_t)seq >= a.n_seqs || len < 0 || (uint64_t)len > a.blocks * a.page_tokens)
             atomicCAS(a.err, 0u, (uint32_t)kErrRange);
     }
     if (nb <= a.n_out) {
-        for (uint32_t i = tid; i < a.n_out; i += kChooseThreads) out[i] = i < nb ? (int32_t)i : -1;
+        for (uint32_t i = tid; i < a.n_out; i += nt) out[i] = i < nb ? (int32_t)i : -1;
         return;
     }
-    float* scores = a.scores + rh * a.blocks;
-    const uint64_t f_end = a.keep_first, l_begin = nb - a.keep_last;  // keep_first + keep_last <= n_out < nb
-    auto kept = [&](uint64_t b) { return b < f_end || b >= l_begin; };
+    const uint32_t f_end = a.keep_first, l_begin = nb - a.keep_last;  // keep_first + keep_last <= n_out < nb
+    // this thread's blocks [at, end)
+    const uint32_t per = (nb + nt - 1) / nt;
+    const uint32_t at = min(tid * per, nb), end = min(at + per, nb);
+    if (KEYS) {
+        if (tid < nb) keys[tid] = order_of(first);
+        for (uint32_t b = tid + nt; b < nb; b += nt) keys[b] = order_of(scores[b]);
+    }
+    for (uint32_t w = tid; w < (nb + 31) / 32; w += nt) near_words[w] = 0;
+    auto key_of = [&](uint32_t b) __attribute__((always_inline)) { return KEYS ? keys[b] : order_of(scores[b]); };
+    auto is_near = [&](uint32_t b) __attribute__((always_inline)) {
+        return ((near_words[b >> 5] >> (b & 31)) & 1u) != 0;
+    };
+    uint32_t turn = 0;
     const uint32_t want = a.n_out - a.keep_first - a.keep_last;
-    uint32_t cut = 0xFFFFFFFFu, ties = 0;  // chosen: above `cut` in order, and the first `ties` equal to it
-    uint32_t nth_key = 0;  // pages that are not near are chosen above this
-    bool any_near = false;
+    // Chosen: keys above `cut`, and the first `ties` equal to it.  Where pages
+    // were summed again, `near` ones among them are those whose mark is left,
+    // or (many of them) those that `cut` and `ties` say, and the others those
+    // above `over`.
+    uint32_t cut = 0xFFFFFFFFu, ties = 0, over = 0xFFFFFFFFu;
+    bool marked = false, ranked = false;
     if (want > 0) {
-        float slack = 0.f;
-        for (uint64_t c = tid; c < (nb + 15) / 16; c += kChooseThreads) slack = fmaxf(slack, a.slack[rh * a.chunks + c]);
-        for (int o = 32; o > 0; o >>= 1) slack = fmaxf(slack, __shfl_xor(slack, o));
-        if (lane == 0) sh.slack[wib] = slack;
-        __syncthreads();
-        for (uint32_t i = 0; i < kChooseWaves; ++i) slack = fmaxf(slack, sh.slack[i]);
-        uint32_t above;
-        const uint32_t nth = nth_largest(
-            nb, want, sh, &above, [&](uint64_t b) { return !kept(b); }, [&](uint64_t b) { return order_of(scores[b]); });
-        const float t = value_of(nth);
-        // Every true score is within `slack` of its sum, so the want-th
-        // largest true one is within slack of t; pages further than two of
-        // them from t are decided, and two more cover the final rounding.
-        const float lo_near = t - 4.f * slack, hi_near = t + 4.f * slack;
-        // with no slack (all products zero, or not finite) the sums are taken as they are
-        const bool finite = t - t == 0.f && slack > 0.f;
-        // pages to be summed again, and how many lie above them
-        for (uint64_t w = tid; w < (nb + 31) / 32; w += kChooseThreads) near_bits[w] = 0;
-        __syncthreads();
-        uint32_t n_above = 0, n_near = 0;
-        for (uint64_t b = tid; b < nb; b += kChooseThreads) {
-            if (kept(b)) continue;
-            const float s = scores[b];
-            if (finite && s >= lo_near && s <= hi_near) {
-                atomicOr(&near_bits[b >> 5], 1u << (b & 31));
-                ++n_near;
-            } else if (order_of(s) > nth) {
-                ++n_above;
-            }
-        }
-        n_above = choose_sum(n_above, sh);
-        n_near = choose_sum(n_near, sh);
-        any_near = finite;
-        if (!finite) {
-            cut = nth;
-            ties = want - above;
-        } else if (n_above + n_near == want) {
-            cut = 0;  // every near one: their keys are above 0, a NaN's
+        if (a.chunks <= nt) {
+            if (tid >= (nb + kWaveBlocks - 1) / kWaveBlocks) slack = 0.f;
         } else {
-            const int64_t* table = a.table + ((uint64_t)seq * a.kv_heads + h) * a.blocks;
-            // one wave per page: lane l sums the dims l, l + 64, ... of every
-            // head of the group in 64 bits
-            for (uint64_t w = wib; w < (nb + 31) / 32; w += kChooseWaves) {
-                for (uint32_t m = uniform(near_bits[w]); m; m &= m - 1) {
-                    const uint64_t b = 32 * w + (uint32_t)__builtin_ctz(m);
-                    const uint32_t id = page_id(table[b], (uint32_t)a.n_slots);
-                    if (id == kNoPage) continue;
-                    const uint16_t* bp = static_cast<const uint16_t*>(a.bounds) + (uint64_t)id * (2ull * D);
-                    float best = -__builtin_inff();
-                    for (uint32_t j = 0; j < a.group; ++j) {
-                        const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (int64_t)r * a.q_row +
-                                             (int64_t)(h * a.group + j) * a.q_head;
-                        double s = 0.0;
-                        for (uint32_t d = lane; d < (uint32_t)D; d += kWave) {
-                            const double x = (double)E::from_bits(qp[d]);
-                            s += (x > 0.0 ? x : 0.0) * (double)E::from_bits(bp[D + d]) +
-                                 (x < 0.0 ? x : 0.0) * (double)E::from_bits(bp[d]);
-                        }
-                        for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-                        best = fmaxf(best, (float)s);
+            slack = 0.f;
+            for (uint32_t c = tid; c < (nb + kWaveBlocks - 1) / kWaveBlocks; c += nt)
+                slack = fmaxf(slack, a.slack[rh * a.chunks + c]);
+        }
+        if (tid == 0) sh.n_near = 0;
+        uint32_t slack_bits = __float_as_uint(slack), zero = 0;
+        choose_max2(slack_bits, zero, sh, turn);  // (and the keys are in LDS)
+        slack = kSumError * __uint_as_float(slack_bits);
+        const uint32_t own_at = max(at, f_end), own_end = min(end, l_begin);
+        auto own = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll 1
+            for (uint32_t b = own_at; b < own_end; ++b) f(b, key_of(b));
+        };
+        auto own_keys = [&](auto f) __attribute__((always_inline)) {
+            own([&](uint32_t, uint32_t k) __attribute__((always_inline)) { f(k); });
+        };
+        uint32_t not_lo = 0, hi = 0;
+        own_keys([&](uint32_t k) __attribute__((always_inline)) {
+            not_lo = max(not_lo, ~k);
+            hi = max(hi, k);
+        });
+        choose_max2(not_lo, hi, sh, turn);
+        const uint32_t lo = ~not_lo;
+        // One pass: the bin of kBins between lo and hi that holds the want-th
+        // largest sum.  Keys of scores that lie close together differ in
+        // their low bits only, so bins are counted from lo.
+        const uint32_t bits = 32 - (uint32_t)__builtin_clz((hi - lo) | 1u), drop = bits > 11 ? bits - 11 : 0u;
+        uint32_t left = want, above;
+        const uint32_t bin = find_bin(kBins, left, sh, turn, [&](auto f) __attribute__((always_inline)) {
+            own_keys([&](uint32_t k) __attribute__((always_inline)) { f((k - lo) >> drop); });
+        });
+        const float t_lo = value_of(lo + (bin << drop));
+        const float t_hi = value_of(min(hi, lo + (bin << drop) + ((1u << drop) - 1)));
+        if (t_lo - t_lo == 0.f && t_hi - t_hi == 0.f && slack > 0.f) {
+            // Every true score is within `slack` of its sum, so the want-th
+            // largest true one lies between t_lo and t_hi widened by slack;
+            // pages that are further than two of them outside are decided
+            // (a third covers the roundings of these bounds and of the score).
+            const uint32_t near_lo = order_of(t_lo - 3.f * slack), near_hi = order_of(t_hi + 3.f * slack);
+            uint32_t n_above = 0, n_near = 0;
+            own([&](uint32_t b, uint32_t k) __attribute__((always_inline)) {
+                if (k > near_hi) {
+                    ++n_above;
+                } else if (k >= near_lo) {
+                    atomicOr(&near_words[b >> 5], 1u << (b & 31));
+                    const uint32_t i = atomicAdd(&sh.n_near, 1u);
+                    if (i < kNearList) sh.near_block[i] = b;
+                    ++n_near;
+                }
+            });
+            const Sums n = choose_sums(n_above, n_near, sh, turn);
+            over = near_hi;
+            if (n.all[0] + n.all[1] == want) {
+                cut = near_lo - 1;  // the near ones are exactly those still wanted
+            } else {
+                const int64_t* table = a.table + ((uint64_t)seq * a.kv_heads + h) * a.blocks;
+                const uint16_t* bounds = static_cast<const uint16_t*>(a.bounds);
+                const uint32_t rest = want - n.all[0];
+                marked = true;
+                if (n.all[1] <= kNearList) {
+                    // the usual case: a few, in a list, ranked by one wave
+                    for (uint32_t i = wib; i < n.all[1]; i += nt / kWave) {
+                        const uint32_t id = page_id(table[uniform(sh.near_block[i])], (uint32_t)a.n_slots);
+                        const uint32_t k =
+                            exact_key<E, D>(a, r, h, bounds + (uint64_t)(id == kNoPage ? 0u : id) * (2ull * D));
+                        if (lane == 0) sh.near_key[i] = k;
                     }
-                    if (lane == 0) scores[b] = best;
-                }
-            }
-            __threadfence_block();
-            __syncthreads();
-            uint32_t above_near;
-            const uint32_t rest = want - n_above;
-            cut = nth_largest(
-                nb, rest, sh, &above_near, [&](uint64_t b) { return ((near_bits[b >> 5] >> (b & 31)) & 1u) != 0; },
-                [&](uint64_t b) { return order_of(scores[b]); });
-            ties = rest - above_near;
-        }
-        nth_key = nth;
-    }
-    // ascending order: a running count over slices of kChooseThreads blocks
-    uint32_t at = 0, ties_used = 0;
-    for (uint64_t base = 0; base < nb; base += kChooseThreads) {
-        const uint64_t b = base + tid;
-        bool in = false, tie = false;
-        if (b < nb) {
-            if (kept(b)) {
-                in = true;
-            } else if (want > 0) {
-                const uint32_t k = order_of(scores[b]);
-                const bool near = any_near && ((near_bits[b >> 5] >> (b & 31)) & 1u);
-                if (any_near && !near) {
-                    in = k > nth_key;
+                    __syncthreads();
+                    if (wib == 0) {
+                        const uint32_t b = lane < n.all[1] ? sh.near_block[lane] : 0u;
+                        const uint32_t k = lane < n.all[1] ? sh.near_key[lane] : 0u;
+                        uint32_t better = 0;
+                        for (uint32_t i = 0; i < n.all[1]; ++i) {
+                            const uint32_t ki = lane_value(k, (int)i), bi = lane_value(b, (int)i);
+                            better += ki > k || (ki == k && bi < b);
+                        }
+                        if (lane < n.all[1] && better >= rest) atomicAnd(&near_words[b >> 5], ~(1u << (b & 31)));
+                    }
+                    __syncthreads();
+                    ranked = true;
                 } else {
-                    in = k > cut;
-                    tie = !in && k == cut;
+                    for (uint32_t w = wib; w < (nb + 31) / 32; w += nt / kWave) {
+                        for (uint32_t m = uniform(near_words[w]); m; m &= m - 1) {
+                            const uint32_t b = 32 * w + (uint32_t)__builtin_ctz(m);
+                            const uint32_t id = page_id(table[b], (uint32_t)a.n_slots);
+                            const uint32_t k =
+                                exact_key<E, D>(a, r, h, bounds + (uint64_t)(id == kNoPage ? 0u : id) * (2ull * D));
+                            if (lane == 0) {
+                                if (KEYS)
+                                    keys[b] = k;
+                                else
+                                    scores[b] = value_of(k);
+                            }
+                        }
+                    }
+                    __threadfence_block();
+                    __syncthreads();
+                    auto near_keys = [&](auto f) __attribute__((always_inline)) {
+                        own([&](uint32_t b, uint32_t k) __attribute__((always_inline)) {
+                            if (is_near(b)) f(k);
+                        });
+                    };
+                    not_lo = hi = 0;
+                    near_keys([&](uint32_t k) __attribute__((always_inline)) {
+                        not_lo = max(not_lo, ~k);
+                        hi = max(hi, k);
+                    });
+                    choose_max2(not_lo, hi, sh, turn);
+                    cut = nth_largest(rest, ~not_lo, hi, sh, turn, &above, near_keys);
+                    ties = rest - above;
                 }
             }
+        } else {
+            // no slack (all products zero, or not finite): the sums as they are
+            cut = nth_largest(want, lo, hi, sh, turn, &above, own_keys);
+            ties = want - above;
         }
-        // ties in order of their block
-        const uint64_t tb = ballot(tie);
-        __syncthreads();
-        if (lane == 0) sh.sums[wib] = (uint32_t)__builtin_popcountll(tb);
-        __syncthreads();
-        uint32_t tie_rank = ties_used + bits_below(tb), slice_ties = 0;
-        for (uint32_t i = 0; i < kChooseWaves; ++i) {
-            if (i < wib) tie_rank += sh.sums[i];
-            slice_ties += sh.sums[i];
-        }
-        ties_used += slice_ties;
-        if (tie && tie_rank < ties) in = true;
-        const uint64_t ib = ballot(in);
-        __syncthreads();
-        if (lane == 0) sh.sums[wib] = (uint32_t)__builtin_popcountll(ib);
-        __syncthreads();
-        uint32_t rank = at + bits_below(ib);
-        for (uint32_t i = 0; i < kChooseWaves; ++i) {
-            if (i < wib) rank += sh.sums[i];
-            at += sh.sums[i];
-        }
-        if (in && rank < a.n_out) out[rank] = (int32_t)b;
     }
-    for (uint32_t i = at + tid; i < a.n_out; i += kChooseThreads) out[i] = -1;
+    // which of this thread's blocks are in, ties in order of their block
+    auto state_of = [&](uint32_t b) __attribute__((always_inline)) -> uint32_t {  // 0 out, 1 in, 2 tie
+        if (b < f_end || b >= l_begin) return 1u;
+        const uint32_t k = key_of(b);
+        if (marked) {
+            const bool near = is_near(b);
+            if (ranked) return near || k > over ? 1u : 0u;
+            if (!near) return k > over ? 1u : 0u;
+        }
+        return k > cut ? 1u : (k == cut ? 2u : 0u);
+    };
+    uint32_t n_ties = 0, n_in = 0;
+#pragma unroll 1
+    for (uint32_t b = at; b < end; ++b) {
+        const uint32_t s = state_of(b);
+        n_in += s == 1u;
+        n_ties += s == 2u;
+    }
+    const Sums n = choose_sums(n_in, n_ties, sh, turn);
+    // rank of this thread's first block: those in front of it, and the ties
+    // in front of it as far as they are taken
+    uint32_t tie_rank = n.before[1], rank = n.before[0] + min(tie_rank, ties);
+    const uint32_t total = n.all[0] + min(n.all[1], ties);
+#pragma unroll 1
+    for (uint32_t b = at; b < end; ++b) {
+        const uint32_t s = state_of(b);
+        if (s == 1u || (s == 2u && tie_rank++ < ties)) {
+            if (rank < a.n_out) out[rank] = (int32_t)b;
+            ++rank;
+        }
+    }
+    for (uint32_t i = total + tid; i < a.n_out; i += nt) out[i] = -1;
 }
 
 }  // namespace ibp
@@ -543,11 +752,12 @@ ibp_status ibp_page_bounds(const ibp_pages* k, uint32_t dtype, uint32_t head_dim
     return from_hip(dtype == IBP_BF16 ? by_size(Bf16{}) : by_size(Fp16{}));
 }
 
-static uint64_t select_chunks(const ibp_attention* a) { return (a->table_blocks + 15) / 16; }
+static uint64_t select_chunks(const ibp_attention* a) { return (a->table_blocks + kWaveBlocks - 1) / kWaveBlocks; }
+static uint64_t select_pitch(const ibp_attention* a) { return (a->table_blocks + 3) & ~3ull; }
 
 uint64_t ibp_select_pages_workspace(const ibp_attention* a) {
     if (!a) return 0;
-    return 4 * a->n_rows * a->n_kv_heads * (a->table_blocks + select_chunks(a)) + 16;
+    return 4 * a->n_rows * a->n_kv_heads * (select_pitch(a) + select_chunks(a));
 }
 
 ibp_status ibp_select_pages(ibp_meta_t h, const ibp_attention* a, const void* q, const void* bounds, uint64_t n_slots,
@@ -568,7 +778,7 @@ ibp_status ibp_select_pages(ibp_meta_t h, const ibp_attention* a, const void* q,
                           (const void*)workspace})
         if (!device_only(p, h->device)) return IBP_ERR_INVALID_ARG;
     if (row_seq && !device_only(row_seq, h->device)) return IBP_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(bounds) % 16 || reinterpret_cast<uintptr_t>(workspace) % 8 ||
+    if (reinterpret_cast<uintptr_t>(bounds) % 16 || reinterpret_cast<uintptr_t>(workspace) % 16 ||
         workspace_bytes < ibp_select_pages_workspace(a))
         return IBP_ERR_INVALID_ARG;
     SelectArgs s{};
@@ -578,9 +788,10 @@ ibp_status ibp_select_pages(ibp_meta_t h, const ibp_attention* a, const void* q,
     s.lens = lens;
     s.row_seq = row_seq;
     s.blocks = a->table_blocks;
+    s.pitch = select_pitch(a);
     s.chunks = select_chunks(a);
     s.scores = static_cast<float*>(workspace);
-    s.slack = s.scores + a->n_rows * a->n_kv_heads * a->table_blocks;
+    s.slack = s.scores + a->n_rows * a->n_kv_heads * s.pitch;
     s.out = blocks;
     s.err = h->d_err;
     s.n_rows = a->n_rows;
@@ -594,24 +805,54 @@ ibp_status ibp_select_pages(ibp_meta_t h, const ibp_attention* a, const void* q,
     s.keep_first = keep_first;
     s.keep_last = keep_last;
     s.n_out = n_blocks;
-    s.rows_per_tile = s.group <= 16 ? 16 / s.group : 1;
-    s.col_tiles = (s.group + 15) / 16;
+    s.pad = 1;
+    while (s.pad < s.group && s.pad < 16) s.pad *= 2;
+    if (s.group > 16) s.pad = (s.group + 15) / 16 * 16;
+    s.log2_pad = s.pad > 16 ? 31 : (uint32_t)__builtin_ctz(s.pad);
+    s.rows_per_tile = s.pad < 16 ? 16 / s.pad : 1;
+    s.head_tiles = s.pad > 16 ? s.pad / 16 : 1;
     s.vec = vectors_ok(q, a->q_row_stride, a->q_head_stride);
-    const uint64_t tiles = (a->n_rows + s.rows_per_tile - 1) / s.rows_per_tile;
-    if (tiles > 65535 || a->n_kv_heads > 65535 || a->n_rows * a->n_kv_heads > 0x7FFFFFFFull) return IBP_ERR_UNSUPPORTED;
+    // Many rows per sequence share the pages' bounds, two tiles of rows a wave
+    // (one of 256 dims, for the registers); few rows take a wave each.
+    const bool shared = a->n_rows >= 4 * a->n_seqs && s.head_tiles == 1;
+    const uint32_t ct = shared && a->head_dim <= 128 ? 2 : 1;
+    s.same_blocks = shared;
+    s.wave_rows = shared ? ct * s.rows_per_tile : 1;
+    // A wave that shares pays for its queries once: as many blocks as leave
+    // about 1,024 workgroups.  (512 rows by 4,096 blocks by 8 heads of 128
+    // dims: 201 us with 64 blocks per wave.)
+    const uint64_t row_groups = (a->n_rows + ct * s.rows_per_tile * kScoreWaves - 1) / (ct * s.rows_per_tile * kScoreWaves);
+    const uint64_t all_chunks = row_groups * a->n_kv_heads * select_chunks(a);
+    s.span = shared ? (uint32_t)std::min<uint64_t>(std::max<uint64_t>(1, all_chunks / 1024), 64) : 1;
+    const uint64_t per_wg_rows = (uint64_t)s.wave_rows * (shared ? kScoreWaves : 1);
+    const uint64_t groups = (a->n_rows + per_wg_rows - 1) / per_wg_rows;
+    if (groups > 65535 || a->n_kv_heads > 65535 || a->n_rows * a->n_kv_heads > 0x7FFFFFFFull)
+        return IBP_ERR_UNSUPPORTED;
     const bool scored = a->table_blocks > n_blocks && n_blocks > keep_first + keep_last;
     auto launch = [&](auto e, auto dc) {
         using E = decltype(e);
         constexpr int D = decltype(dc)::value;
         if (scored) {  // no row can have more pages than it may read otherwise
-            const dim3 grid((uint32_t)((a->table_blocks + kScoreChunk - 1) / kScoreChunk), a->n_kv_heads,
-                            (uint32_t)tiles);
-            hipLaunchKernelGGL((k_scores<E, D>), grid, dim3(kWave * kScoreWaves), 0, stream, s);
+            const uint64_t per_wg = (uint64_t)(shared ? 1 : kScoreWaves) * kWaveBlocks * s.span;
+            const dim3 grid((uint32_t)((a->table_blocks + per_wg - 1) / per_wg), a->n_kv_heads, (uint32_t)groups);
+            if (shared)
+                hipLaunchKernelGGL((k_scores<E, D, D == 256 ? 1 : 2>), grid, dim3(kWave * kScoreWaves), 0, stream, s);
+            else
+                hipLaunchKernelGGL((k_scores<E, D, 1>), grid, dim3(kWave * kScoreWaves), 0, stream, s);
             const hipError_t err = hipGetLastError();
             if (err != hipSuccess) return err;
         }
-        hipLaunchKernelGGL((k_choose<E, D>), dim3((uint32_t)(a->n_rows * a->n_kv_heads)), dim3(kChooseThreads),
-                           (uint32_t)(4 * ((a->table_blocks + 31) / 32)), stream, s);
+        const dim3 grid((uint32_t)(a->n_rows * a->n_kv_heads));
+        const uint32_t marks = (uint32_t)(4 * ((a->table_blocks + 31) / 32));
+        if (a->table_blocks <= kLdsKeys) {
+            // eight blocks per thread
+            const uint32_t waves =
+                (uint32_t)std::min<uint64_t>(16, std::max<uint64_t>(4, (a->table_blocks + 8 * kWave - 1) / (8 * kWave)));
+            hipLaunchKernelGGL((k_choose<E, D, true>), grid, dim3(kWave * waves),
+                               marks + (uint32_t)(4 * a->table_blocks), stream, s);
+        } else {
+            hipLaunchKernelGGL((k_choose<E, D, false>), grid, dim3(1024), marks, stream, s);
+        }
         return hipGetLastError();
     };
     auto by_dim = [&](auto e) {
