@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "../../include/ibp.h"
 #include "ibp_attention.hpp"
@@ -115,7 +116,9 @@ ibp_status fill_args(const ibp_pages* k, const ibp_pages* v, const ibp_attention
     x->row_tiles = p.row_tiles;
     x->work = (uint32_t)(items * a->n_kv_heads);
     x->q_vec = vectors_ok(q, a->q_row_stride, a->q_head_stride);
-    x->scale2 = a->scale * kLog2e;
+    // a scale of zero weighs all keys alike; masked scores stay -infinity
+    x->scale2 = std::max(std::fabs(a->scale) * kLog2e, 1e-30f);
+    x->q_sign = a->scale < 0.f ? 0x80008000u : 0u;
     // Tables in LDS where they fit; large ones otherwise stay in device memory
     // (small ones, of fewer than four positions, always fit).
     x->same_tab = k->meta == v->meta;

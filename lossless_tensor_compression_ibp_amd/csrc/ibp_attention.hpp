@@ -61,7 +61,8 @@ struct AttnArgs {
     uint32_t tab_words_k, tab_words_v;  // LDS words of the tables (0: not staged)
     uint32_t tab_lds_k, tab_lds_v;      // staged in LDS, else read where they lie in device memory
     uint32_t same_tab;                  // values have the keys' tables
-    float scale2;              // scale * log2(e)
+    float scale2;              // |scale| * log2(e), not zero
+    uint32_t q_sign;           // both sign bits for a negative scale
 };
 
 typedef short i16x4 __attribute__((ext_vector_type(4)));
@@ -91,6 +92,20 @@ struct AttnShape {
         kAttnWaves * wave_bytes + shared_bytes > join_bytes ? kAttnWaves * wave_bytes + shared_bytes : join_bytes;
 };
 
+// Infinities and NaNs of eight numbers become zero; whether there was one.
+template <class E>
+__device__ __forceinline__ bool clear_odd(u32x4& x) {
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = x[j] & E::kExponent, hi = (x[j] >> 16) & E::kExponent;
+        if (lo == E::kExponent) x[j] &= 0xFFFF0000u;
+        if (hi == E::kExponent) x[j] &= 0x0000FFFFu;
+        odd = odd || lo == E::kExponent || hi == E::kExponent;
+    }
+    return odd;
+}
+
 __device__ __forceinline__ void lds_order() { asm volatile("" ::: "memory"); }
 
 template <class E, int D, int T, int MR, bool SHARED, bool TREE>
@@ -99,10 +114,18 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
     using V8 = typename E::V8;
     constexpr int NV = S::NV, STEP = S::STEP, PP = S::PP, PW = S::PW, TILES = S::CHUNK / 16;
     constexpr int DK = D / 32, DN = D / 16;
-    extern __shared__ uint32_t smem[];
+    extern __shared__ __align__(16) uint32_t smem[];
     __shared__ float join_m[kAttnWaves][16], join_l[kAttnWaves][16];
+    __shared__ uint32_t odd_values;  // an infinity or NaN among the drafted values
     const uint32_t lane = lane_id(), wib = uniform(threadIdx.x / kWave);
     const uint32_t col = lane & 15u, g = lane >> 4;
+
+    // the first vector per thread of each pool's tables is on its way while
+    // the wave finds its pages
+    u32x4 tab_k = {0u, 0u, 0u, 0u}, tab_v = {0u, 0u, 0u, 0u};
+    if (4 * threadIdx.x < a.tab_words_k) tab_k = page_table_vector(a.k, threadIdx.x);
+    if (4 * threadIdx.x < a.tab_words_v) tab_v = page_table_vector(a.v, threadIdx.x);
+    if (TREE && threadIdx.x == 0) odd_values = 0;
 
     // which part of the work: split, (sequence or row, head), row tile
     const uint32_t split = blockIdx.x % a.splits;
@@ -146,10 +169,6 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
     constexpr uint32_t kStride = SHARED ? 1u : kAttnWaves;
     const uint32_t n_steps = s_first < s_hi ? (s_hi - s_first + kStride - 1) / kStride : 0u;
 
-    // tables of the record formats
-    if (a.tab_lds_k) stage_page_tables(a.k, smem);
-    if (a.tab_lds_v && !a.same_tab) stage_page_tables(a.v, smem + a.tab_words_k);
-    __syncthreads();
     char* const area = reinterpret_cast<char*>(smem + a.tab_words_k + a.tab_words_v);
     uint32_t* const stage = reinterpret_cast<uint32_t*>(area + wib * S::wave_bytes);
     char* const k_tile =
@@ -195,7 +214,11 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
             }
         }
     };
-    // page p of local step i -> registers; draft steps read the dense rows
+    // Page p of local step i -> registers.  Draft steps read the dense rows;
+    // their values' infinities and NaNs are taken out here, so that they reach
+    // no row through a product with a weight of zero, and added at the end to
+    // the rows that see them (add_odd_values).
+    bool odd = false;
     auto load = [&](u32x4* st, uint32_t i, bool values, uint32_t slot_lo) __attribute__((always_inline)) {
         const uint32_t s = s_first + i * kStride;
 #pragma unroll
@@ -210,6 +233,7 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
                     dst[r] = u32x4{0u, 0u, 0u, 0u};
                     if (token < n_new)
                         dst[r] = load_eight(base + (int64_t)(first_row + token) * a.new_row + d, a.new_vec != 0);
+                    if (values) odd |= clear_odd<E>(dst[r]);
                 }
             } else {
                 load_page<NV>(dst, values ? a.v.slots : a.k.slots,
@@ -258,8 +282,8 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
         const uint16_t* qp = a.q + (int64_t)q_row[t] * a.q_row + (int64_t)(h * a.group + j) * a.q_head;
 #pragma unroll
         for (int kk = 0; kk < DK; ++kk) {
-            const u32x4 x = q_on[t] ? load_eight(qp + 32 * kk + 8 * g, a.q_vec != 0) : u32x4{0u, 0u, 0u, 0u};
-            qf[t][kk] = bits_as<V8>(x);
+            u32x4 x = q_on[t] ? load_eight(qp + 32 * kk + 8 * g, a.q_vec != 0) : u32x4{0u, 0u, 0u, 0u};
+            qf[t][kk] = bits_as<V8>(x ^ a.q_sign);  // (a negative scale is taken into the queries)
         }
         m[t] = -__builtin_inff();
         l[t] = 0.f;
@@ -273,6 +297,12 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
         load(st_a, 0, only_v, id_a);
         if (S::BOTH && !S::ONE) load(st_b, 0, true, id_b);
     }
+    // tables of the record formats
+    if (4 * threadIdx.x < a.tab_words_k) reinterpret_cast<u32x4*>(smem)[threadIdx.x] = tab_k;
+    if (4 * threadIdx.x < a.tab_words_v) reinterpret_cast<u32x4*>(smem + a.tab_words_k)[threadIdx.x] = tab_v;
+    if (a.tab_words_k) stage_page_tables(a.k, smem, kWave * kAttnWaves);
+    if (a.tab_words_v) stage_page_tables(a.v, smem + a.tab_words_k, kWave * kAttnWaves);
+    __syncthreads();
     for (uint32_t i = 0; i < n_steps; ++i) {
         const uint32_t s = s_first + i * kStride;
         const bool draft = TREE && s >= ctx_steps;
@@ -365,7 +395,7 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
                 for (int t = 0; t < MR; ++t) sc[t][u] = E::mfma(kf, qf[t][kk], sc[t][u]);
             }
         }
-        // scaled scores, masked ones -infinity; bit 4 u + e of `seen` (drafts)
+        // masked scores -infinity, the running maximum, weights
         bool whole = !draft;
 #pragma unroll
         for (int u = 0; u < TILES; ++u) whole = whole && tile_held(u) >= 16u;
@@ -382,21 +412,21 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
             float top = -__builtin_inff();
 #pragma unroll
             for (int u = 0; u < TILES; ++u) {
-                const uint32_t n = tile_held(u);
+                if (!whole) {
+                    const uint32_t n = tile_held(u);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = sc[t][u][e] * a.scale2;
-                    if (!whole) {
+                    for (int e = 0; e < 4; ++e) {
                         bool on = 4 * g + e < n;
                         if (draft) on = on && ((seen[u >> 1] >> (16 * (u & 1) + 4 * g + e)) & 1u);
-                        x = on ? x : -__builtin_inff();
+                        sc[t][u][e] = on ? sc[t][u][e] : -__builtin_inff();
                     }
-                    sc[t][u][e] = x;
-                    top = fmaxf(top, x);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[t][u][e]);
             }
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
+            top *= a.scale2;
             // The maximum is moved only when a score passes it by more than
             // 8 (weights then stay below 2^8 and sums far from overflow), so
             // most steps rescale nothing.
@@ -408,12 +438,12 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
 #pragma unroll
                 for (int n = 0; n < DN; ++n) o[t][n] *= f;
             }
-            const float base = m[t] == -__builtin_inff() ? 0.f : m[t];
+            const float base = m[t] == -__builtin_inff() ? 0.f : -m[t];
 #pragma unroll
             for (int u = 0; u < TILES; ++u) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float p = __builtin_amdgcn_exp2f(sc[t][u][e] - base);
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][u][e], a.scale2, base));
                     sc[t][u][e] = p;
                     l[t] += p;
                 }
@@ -428,46 +458,7 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
             process(st_b, true, 1, v_tile, S::RV);
             if (more) load(st_b, i + 1, true, next_b);
         }
-        // A drafted value that is infinite or NaN must not reach the rows that
-        // do not see its token through a product with zero: such a step is
-        // summed token by token, over the tokens that a row sees.
-        bool odd = false;
-        if (draft) {
-            for (uint32_t w = lane; w < S::CHUNK * (D / 2); w += kWave) {
-                const uint32_t x = *reinterpret_cast<const uint32_t*>(vt + (w / (D / 2)) * S::RV + 4 * (w % (D / 2)));
-                odd |= (x & E::kExponent) == E::kExponent || ((x >> 16) & E::kExponent) == E::kExponent;
-            }
-            odd = ballot(odd) != 0;
-        }
-        if (TREE && odd) {
-#pragma unroll
-            for (int t = 0; t < MR; ++t) {
-#pragma unroll
-                for (int u = 0; u < TILES; ++u) {
-                    const uint32_t word = (s - ctx_steps) * (STEP / 32) + t0 / 32 + (u >> 1);
-                    const uint32_t vis = q_on[t] && word < a.mask_words2
-                                             ? a.mask[q_row[t] * a.mask_words2 + word] >> (16 * (u & 1))
-                                             : 0u;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-#pragma unroll 1
-                        for (uint32_t gs = 0; gs < 4; ++gs) {
-                            const uint32_t token = 4 * gs + e;
-                            const float p = __shfl(sc[t][u][e], (int)(16 * gs + col));
-                            const bool on = ((vis >> token) & 1u) && token < tile_held(u);
-#pragma unroll
-                            for (int n = 0; n < DN; ++n) {
-                                const u32x2 x = *reinterpret_cast<const u32x2*>(
-                                    vt + (16 * u + token) * S::RV + 32 * n + 8 * g);
-#pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    if (on) o[t][n][c] += p * E::from_bits(x[c >> 1] >> (16 * (c & 1)));
-                            }
-                        }
-                    }
-                }
-            }
-        } else {
+        {
 #pragma unroll
             for (int u = 0; u < TILES; u += 2) {
                 V8 pf[MR];
@@ -550,6 +541,37 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
                 }
                 const uint32_t i = rho / a.group, j = rho - i * a.group;
                 finish(first_row + i, h * a.group + j, d, x, mm, ll);
+            }
+        }
+    }
+    if constexpr (TREE) {
+        // Drafted values that are infinite or NaN: added to what the rows
+        // that see them have in memory.
+        if (ballot(odd) && lane == 0) odd_values = 1;
+        __syncthreads();
+        if (odd_values) {
+            const uint32_t j_lo = s_lo > ctx_steps ? (s_lo - ctx_steps) * STEP : 0u;
+            const uint32_t j_hi = s_hi > ctx_steps ? min((s_hi - ctx_steps) * STEP, n_new) : 0u;
+            const uint32_t n_rows = min(rows - rt * kRowsWg, kRowsWg);
+            for (uint32_t e = threadIdx.x; e < n_rows * D; e += kWave * kAttnWaves) {
+                const uint32_t rho = rt * kRowsWg + e / D, d = e % D;
+                const uint32_t i = rho / a.group, j = rho - i * a.group;
+                const uint64_t row = first_row + i;
+                float sum = 0.f;
+                bool any = false;
+                for (uint32_t k = j_lo; k < j_hi; ++k) {
+                    if (!((a.mask[row * a.mask_words2 + k / 32] >> (k % 32)) & 1u)) continue;
+                    const uint32_t v = a.v_new[(int64_t)(first_row + k) * a.new_row + (int64_t)h * a.new_head + d];
+                    if ((v & E::kExponent) != E::kExponent) continue;
+                    sum += E::from_bits(v);
+                    any = true;
+                }
+                if (!any) continue;
+                const uint64_t rh = row * nq + h * a.group + j;
+                if (a.splits == 1)
+                    a.out[rh * D + d] = (uint16_t)E::pack(E::from_bits(a.out[rh * D + d]) + sum, 0.f);
+                else
+                    a.part[(rh * a.splits + split) * D + d] += sum;
             }
         }
     }

@@ -50,16 +50,30 @@ __host__ __device__ constexpr uint32_t page_tab_words(uint32_t Mw, uint32_t runs
     return (2u + page_dx_rows(runs) + runs) * page_tab_stride(Mw);
 }
 
-// Whole workgroup: the pool's tables into lds.  The caller synchronises.
-__device__ __forceinline__ void stage_page_tables(const Pool& p, uint32_t* lds) {
-    const uint32_t S = page_tab_stride(p.Mw), dxr = page_dx_rows(p.runs), n = page_tab_words(p.Mw, p.runs);
-    for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
-        const uint32_t row = i / S, pos = (i - row * S) & (p.Mw - 1);  // Mw is a power of two
-        const uint32_t* src = row == 0 ? p.t.kd
-                              : row == 1 ? p.t.b
-                              : row < 2 + dxr ? p.t.dx + (row - 2) * p.src_Mw
-                                              : p.t.r + (row - 2 - dxr) * p.src_Mw;
-        lds[i] = src[pos];
+// Vector i (four words) of the pool's tables as they stand in LDS.
+__device__ __forceinline__ u32x4 page_table_vector(const Pool& p, uint32_t i) {
+    const uint32_t S = page_tab_stride(p.Mw), dxr = page_dx_rows(p.runs);
+    const uint32_t row = (4 * i) >> (31 - __builtin_clz(S)), pos = (4 * i) & (S - 1);  // periods are powers of two
+    const uint32_t* src = row == 0 ? p.t.kd
+                          : row == 1 ? p.t.b
+                          : row < 2 + dxr ? p.t.dx + (row - 2) * p.src_Mw
+                                          : p.t.r + (row - 2 - dxr) * p.src_Mw;
+    if (p.Mw >= 4) return *reinterpret_cast<const u32x4*>(src + pos);
+    const uint32_t x = src[0], y = src[p.Mw - 1];
+    return u32x4{x, y, x, y};
+}
+
+// Whole workgroup: vectors [from, page_tab_words / 4) of the pool's tables
+// into lds, four loads of a thread in flight.  The caller synchronises.
+__device__ __forceinline__ void stage_page_tables(const Pool& p, uint32_t* lds, uint32_t from = 0) {
+    const uint32_t n = page_tab_words(p.Mw, p.runs) / 4;
+    for (uint32_t i = from + threadIdx.x; i < n; i += 4 * blockDim.x) {
+        u32x4 v[4];
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u) v[u] = page_table_vector(p, min(i + u * blockDim.x, n - 1));
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u)
+            if (i + u * blockDim.x < n) reinterpret_cast<u32x4*>(lds)[i + u * blockDim.x] = v[u];
     }
 }
 

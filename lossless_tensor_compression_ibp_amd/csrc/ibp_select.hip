@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kWave * kBoundWaves) void k_page_bounds(Pool pool, 
                                                                      const int64_t* __restrict__ ids,
                                                                      const int32_t* __restrict__ tokens, uint64_t n,
                                                                      uint32_t* __restrict__ bounds) {
-    extern __shared__ uint32_t smem[];
+    extern __shared__ __align__(16) uint32_t smem[];
     const uint32_t lane = lane_id(), wib = uniform(threadIdx.x / kWave);
     const uint32_t tab_words = TAB_LDS ? page_tab_words(pool.Mw, pool.runs) : 0u;
     if (TAB_LDS) {
@@ -500,7 +500,7 @@ __device__ __forceinline__ uint32_t exact_key(const SelectArgs& a, uint64_t r, u
 template <class E, int D, bool KEYS>
 __global__ __launch_bounds__(1024) void k_choose(SelectArgs a) {
     __shared__ ChooseShared sh;
-    extern __shared__ uint32_t smem[];
+    extern __shared__ __align__(16) uint32_t smem[];
     uint32_t* const near_words = smem;  // blocks to be summed in 64 bits
     uint32_t* const keys = smem + (a.blocks + 31) / 32;
     const uint64_t rh = blockIdx.x;
