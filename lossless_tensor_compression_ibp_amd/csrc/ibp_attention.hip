@@ -115,7 +115,6 @@ ibp_status fill_args(const ibp_pages* k, const ibp_pages* v, const ibp_attention
     x->splits = p.splits;
     x->row_tiles = p.row_tiles;
     x->work = (uint32_t)(items * a->n_kv_heads);
-    x->q_vec = vectors_ok(q, a->q_row_stride, a->q_head_stride);
     // a scale of zero weighs all keys alike; masked scores stay -infinity
     x->scale2 = std::max(std::fabs(a->scale) * kLog2e, 1e-30f);
     x->q_sign = a->scale < 0.f ? 0x80008000u : 0u;
@@ -163,7 +162,7 @@ ibp_status ibp_tree_attention(const ibp_pages* k, const ibp_pages* v, const ibp_
     if (st != IBP_OK) return st;
     if (a->n_rows == 0) return IBP_OK;
     if (a->max_new == 0 || mask_words == 0 || mask_words > (1u << 20) || a->max_new > (1u << 20) ||
-        a->new_row_stride < 0 || a->new_head_stride < 0)
+        a->new_row_stride < 0 || a->new_head_stride < 0 || a->new_row_stride >= (1ll << 30))
         return IBP_ERR_INVALID_ARG;
     for (const void* p : {(const void*)new_rows, k_new, v_new, (const void*)mask})
         if (!device_only(p, dev)) return IBP_ERR_INVALID_ARG;
@@ -181,8 +180,6 @@ ibp_status ibp_tree_attention(const ibp_pages* k, const ibp_pages* v, const ibp_
     x.max_new = a->max_new;
     x.new_row = a->new_row_stride;
     x.new_head = a->new_head_stride;
-    x.new_vec = vectors_ok(k_new, a->new_row_stride, a->new_head_stride) &
-                vectors_ok(v_new, a->new_row_stride, a->new_head_stride);
     return launch(x, p, a, true, lds, stream);
 }
 

@@ -57,7 +57,6 @@ struct AttnArgs {
     int64_t q_row, q_head, new_row, new_head;
     uint32_t n_list, mask_words2, max_new;
     uint32_t kv_heads, group, splits, row_tiles, work;  // work: (sequence or row) * kv_heads
-    uint32_t q_vec, new_vec;
     uint32_t tab_words_k, tab_words_v;  // LDS words of the tables (0: not staged)
     uint32_t tab_lds_k, tab_lds_v;      // staged in LDS, else read where they lie in device memory
     uint32_t same_tab;                  // values have the keys' tables
@@ -85,7 +84,8 @@ struct AttnShape {
     static constexpr uint32_t stage_bytes = 4 * page_stage_words<NV>();
     static constexpr int CHUNK = SHARED ? 64 : STEP;       // tokens per pass of the softmax
     static constexpr bool ONE = !SHARED && PW * NV > 8;    // one register buffer for keys and values in turn
-    static constexpr uint32_t wave_bytes = (stage_bytes + 15) / 16 * 16 + (SHARED ? 0 : STEP * RV);
+    static constexpr uint32_t wave_bytes = PW * stage_bytes + (SHARED ? 0 : STEP * RV);
+    static_assert(stage_bytes % 16 == 0, "areas are vectors");
     static constexpr uint32_t shared_bytes = SHARED ? STEP * (RK + RV) : 0;
     static constexpr uint32_t join_bytes = SHARED ? 0 : kAttnWaves * (16 * (D + 4) * 4);
     static constexpr uint32_t area_bytes =
@@ -108,12 +108,25 @@ __device__ __forceinline__ bool clear_odd(u32x4& x) {
 
 __device__ __forceinline__ void lds_order() { asm volatile("" ::: "memory"); }
 
+// The kernel's arguments once more.  What only rare or final steps need is
+// read through this pointer where it is needed: the compiler cannot tell that
+// it is the arguments', so it does not keep them in scalar registers (with all
+// of them live the loop spent a tenth of its instructions on saving them).
+typedef const __attribute__((address_space(4))) AttnArgs* ArgsPtr;
+__device__ __forceinline__ ArgsPtr args_again() {
+    ArgsPtr p = (ArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return p;
+}
+
 template <class E, int D, int T, int MR, bool SHARED, bool TREE>
 __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
     using S = AttnShape<D, T, SHARED>;
     using V8 = typename E::V8;
     constexpr int NV = S::NV, STEP = S::STEP, PP = S::PP, PW = S::PW, TILES = S::CHUNK / 16;
     constexpr int DK = D / 32, DN = D / 16;
+    constexpr uint32_t kRowsWg = 16u * MR * (SHARED ? kAttnWaves : 1u);
+    constexpr uint32_t kStride = SHARED ? 1u : kAttnWaves;  // steps between a wave's steps
     extern __shared__ __align__(16) uint32_t smem[];
     __shared__ float join_m[kAttnWaves][16], join_l[kAttnWaves][16];
     __shared__ uint32_t odd_values;  // an infinity or NaN among the drafted values
@@ -131,23 +144,24 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
     const uint32_t split = blockIdx.x % a.splits;
     const uint32_t wg = (blockIdx.x / a.splits) % a.work, rt = blockIdx.x / a.splits / a.work;
     const uint32_t h = wg % a.kv_heads;
-    const uint64_t item = wg / a.kv_heads;  // sequence (tree) or row
-    int64_t seq = TREE ? (int64_t)item : (a.row_seq ? (int64_t)a.row_seq[item] : (int64_t)item);
-    int64_t len = a.lens[item];
-    uint64_t first_row = TREE ? 0 : item;
-    uint32_t n_new = TREE ? 0 : 1;
-    bool bad = seq < 0 || (uint64_t)seq >= a.n_seqs || len < 0;
+    const uint32_t item = wg / a.kv_heads;  // sequence (tree) or row
+    uint32_t seq = item, first_row = TREE ? 0u : item, n_new = TREE ? 0u : 1u;
+    int32_t len = a.lens[item];
+    bool bad = len < 0 || (uint64_t)len > a.table_blocks * T;
     if (TREE) {
-        const int64_t r0 = a.new_rows[item], r1 = a.new_rows[item + 1];
-        if (r0 < 0 || r1 < r0 || (uint64_t)r1 > a.n_rows || r1 - r0 > (int64_t)a.max_new ||
-            (uint64_t)(r1 - r0) > 32ull * a.mask_words2) {
+        const int32_t r0 = a.new_rows[item], r1 = a.new_rows[item + 1];
+        const uint32_t n = (uint32_t)(r1 - r0);
+        if (r0 < 0 || r1 < r0 || (uint64_t)r1 > a.n_rows || n > a.max_new || n > 32u * a.mask_words2) {
             bad = true;
         } else {
-            first_row = (uint64_t)r0;
-            n_new = (uint32_t)(r1 - r0);
+            first_row = (uint32_t)r0;
+            n_new = n;
         }
+    } else if (a.row_seq) {
+        const int32_t s = a.row_seq[item];
+        bad = bad || s < 0 || (uint64_t)s >= a.n_seqs;
+        seq = (uint32_t)s;
     }
-    if (!bad && (uint64_t)len > a.table_blocks * T) bad = true;
     if (bad) {
         latch_error(a.k.err, kErrRange);
         if (TREE) return;
@@ -155,24 +169,22 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
         len = 0;
     }
     const uint32_t rows = n_new * a.group;
-    constexpr uint32_t kRowsWg = 16u * MR * (SHARED ? kAttnWaves : 1u);
     if (rt * kRowsWg >= rows) return;
     const uint32_t row0 = rt * kRowsWg + (SHARED ? wib * 16u * MR : 0u);
 
     // steps of this split: the context's, then the drafted tokens'
-    const uint32_t ctx_pages = TREE ? (uint32_t)((len + T - 1) / T) : (len > 0 ? a.n_list : 0u);
+    const uint32_t ctx_pages = TREE ? ((uint32_t)len + T - 1) / T : (len > 0 ? a.n_list : 0u);
     const uint32_t ctx_steps = (ctx_pages + PP - 1) / PP;
     const uint32_t all_steps = ctx_steps + (TREE ? (n_new + STEP - 1) / STEP : 0u);
     const uint32_t per = (all_steps + a.splits - 1) / a.splits;
     const uint32_t s_lo = min(split * per, all_steps), s_hi = min(s_lo + per, all_steps);
     const uint32_t s_first = s_lo + (SHARED ? 0u : wib);
-    constexpr uint32_t kStride = SHARED ? 1u : kAttnWaves;
     const uint32_t n_steps = s_first < s_hi ? (s_hi - s_first + kStride - 1) / kStride : 0u;
 
     char* const area = reinterpret_cast<char*>(smem + a.tab_words_k + a.tab_words_v);
     uint32_t* const stage = reinterpret_cast<uint32_t*>(area + wib * S::wave_bytes);
     char* const k_tile =
-        SHARED ? area + kAttnWaves * S::wave_bytes : reinterpret_cast<char*>(stage) + (S::stage_bytes + 15) / 16 * 16;
+        SHARED ? area + kAttnWaves * S::wave_bytes : reinterpret_cast<char*>(stage) + PW * S::stage_bytes;
     char* const v_tile = SHARED ? k_tile + STEP * S::RK : k_tile;
 
     // a wave of SHARED pages of 32 or 64 tokens loads keys or values only
@@ -180,285 +192,327 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
     const uint32_t page_in_step = SHARED ? (T == 16 ? wib : wib >> 1) : 0u;
 
     // --- the wave's next pages: lane l has page l % PW of its step base + l / PW
-    uint32_t id_a = kNoPage, id_b = kNoPage, held = 0, comp = 0;
-    const int32_t* list = TREE ? nullptr : a.blocks + (item * a.kv_heads + h) * a.n_list;
-    const uint64_t table_row = ((uint64_t)seq * a.kv_heads + h) * a.table_blocks;
+    uint32_t id_a = 0, id_b = 0, held = 0, comp = 0;
     auto refill = [&](uint32_t base) __attribute__((always_inline)) {
+        const ArgsPtr c = args_again();
         const uint32_t s = s_first + (base + lane / PW) * kStride;
-        id_a = id_b = kNoPage;
-        held = comp = 0;
+        id_a = id_b = held = comp = 0;
         if (s < s_hi && s < ctx_steps) {
             const uint32_t n = s * PP + (SHARED ? page_in_step : lane % PW);
-            int64_t block = n < ctx_pages ? (TREE ? (int64_t)n : (int64_t)list[n]) : -1;
-            if (block >= 0 && block * T < len) {
-                held = (uint32_t)min((int64_t)T, len - block * T);
+            int32_t block = n < ctx_pages ? (int32_t)n : -1;
+            if (!TREE && n < ctx_pages) block = c->blocks[((uint64_t)item * a.kv_heads + h) * c->n_list + n];
+            if (block >= 0 && (int64_t)block * T < len) {
+                held = (uint32_t)min(T, len - block * T);
+                const uint64_t at = ((uint64_t)seq * a.kv_heads + h) * c->table_blocks + (uint32_t)block;
                 bool missing = false;
-                if (S::BOTH || !only_v) {
-                    id_a = page_id(a.k_table[table_row + block], a.k.n_slots);
-                    missing = id_a == kNoPage;
-                    if (!missing) comp = page_bit(a.k.bitmask, id_a);
-                }
-                if (S::BOTH || only_v) {
-                    const uint32_t id = page_id(a.v_table[table_row + block], a.v.n_slots);
-                    missing |= id == kNoPage;
-                    const uint32_t bit = id == kNoPage ? 0u : page_bit(a.v.bitmask, id);
-                    if (S::BOTH) {
-                        id_b = id;
-                        comp |= bit << 1;
-                    } else {
-                        id_a = id;
-                        comp = bit;
+                auto find = [&](const int64_t* table, uint32_t n_slots, const uint32_t* bitmask, uint32_t shift)
+                                __attribute__((always_inline)) -> uint32_t {
+                    const uint32_t id = page_id(table[at], n_slots);
+                    if (id == kNoPage) {
+                        missing = true;
+                        return 0u;
                     }
-                }
-                if (missing) atomicCAS(a.k.err, 0u, (uint32_t)kErrRange);
+                    comp |= page_bit(bitmask, id) << shift;
+                    return id;
+                };
+                if (S::BOTH || !only_v) id_a = find(c->k_table, c->k.n_slots, c->k.bitmask, 0);
+                if (S::BOTH) id_b = find(c->v_table, c->v.n_slots, c->v.bitmask, 1);
+                if (!S::BOTH && only_v) id_a = find(c->v_table, c->v.n_slots, c->v.bitmask, 0);
+                if (missing) atomicCAS(c->k.err, 0u, (uint32_t)kErrRange);
             }
         }
     };
-    // Page p of local step i -> registers.  Draft steps read the dense rows;
-    // their values' infinities and NaNs are taken out here, so that they reach
-    // no row through a product with a weight of zero, and added at the end to
-    // the rows that see them (add_odd_values).
-    bool odd = false;
-    auto load = [&](u32x4* st, uint32_t i, bool values, uint32_t slot_lo) __attribute__((always_inline)) {
+    // Page p of local step i -> registers: T rows of D numbers, of a slot, or
+    // of the drafted tokens' dense rows (where rows past the last token read
+    // the last one).  What they hold beyond the page's tokens is masked (keys)
+    // or cleared (values) later.
+    auto load = [&](u32x4* st, uint32_t i, bool values, uint32_t ids) __attribute__((always_inline)) {
         const uint32_t s = s_first + i * kStride;
 #pragma unroll
         for (int p = 0; p < PW; ++p) {
-            u32x4* dst = st + p * NV;
+            const uint32_t id = lane_value(ids, (int)((i % (64 / PW)) * PW + p));
+            const uint8_t* base = (values ? a.v.slots : a.k.slots) + (uint64_t)id * (uint64_t)(2 * D * T);
+            uint32_t row_bytes = 2 * D, last = T - 1;
             if (TREE && s >= ctx_steps) {
-                const uint32_t j0 = (s - ctx_steps) * STEP + (SHARED ? page_in_step : (uint32_t)p) * T;
-                const uint16_t* base = (values ? a.v_new : a.k_new) + (int64_t)h * a.new_head;
+                const ArgsPtr c = args_again();
+                const uint32_t j0 = min((s - ctx_steps) * STEP + (SHARED ? page_in_step : (uint32_t)p) * T, n_new - 1);
+                base = reinterpret_cast<const uint8_t*>((values ? c->v_new : c->k_new) + (int64_t)h * c->new_head +
+                                                        (int64_t)(first_row + j0) * c->new_row);
+                row_bytes = (uint32_t)c->new_row * 2u;
+                last = min(last, n_new - 1 - j0);
+            }
 #pragma unroll
-                for (int r = 0; r < NV; ++r) {
-                    const uint32_t w = 256u * r + 4u * lane, token = j0 + w / (D / 2), d = 2 * (w % (D / 2));
-                    dst[r] = u32x4{0u, 0u, 0u, 0u};
-                    if (token < n_new)
-                        dst[r] = load_eight(base + (int64_t)(first_row + token) * a.new_row + d, a.new_vec != 0);
-                    if (values) odd |= clear_odd<E>(dst[r]);
-                }
-            } else {
-                load_page<NV>(dst, values ? a.v.slots : a.k.slots,
-                              lane_value(slot_lo, (int)((i % (64 / PW)) * PW + p)));
+            for (int r = 0; r < NV; ++r) {
+                const uint32_t w = 256u * r + 4u * lane, token = min(w / (D / 2), last), b = 4 * (w % (D / 2));
+                typedef u32x4 u32x4_any __attribute__((aligned(2)));
+                st[p * NV + r] = *reinterpret_cast<const u32x4_any*>(base + (uint64_t)token * row_bytes + b);
             }
         }
     };
-    // Page p of the wave as rows of tokens in LDS, rebuilt if it is a record;
-    // values behind its last token become zero.
-    auto put = [&](const u32x4* st, int p, bool values, bool record, uint32_t n, char* tile, int stride)
+    // The wave's pages as rows of tokens in LDS.  A record goes through the
+    // stage; values behind a page's last token become zero.  Lane-wise words
+    // of a page: four at w, of token w / (D / 2).
+    auto put = [&](const u32x4* st, bool values, uint32_t records, const uint32_t* keep, char* tile, int stride)
                    __attribute__((always_inline)) {
-        char* const to = tile + (SHARED ? page_in_step : (uint32_t)p) * (T * stride);
-        const uint32_t keep = values ? n : (uint32_t)T;
-        auto sink = [&](uint32_t w, u32x4 x) __attribute__((always_inline)) {
+        auto row_of = [&](uint32_t p, uint32_t n, uint32_t w, u32x4 x) __attribute__((always_inline)) {
             const uint32_t token = w / (D / 2), b = 4 * (w % (D / 2));
-            if (token >= keep) x = u32x4{0u, 0u, 0u, 0u};
-            *reinterpret_cast<u32x4*>(to + token * stride + b) = x;
+            if (token >= n) x = u32x4{0u, 0u, 0u, 0u};
+            *reinterpret_cast<u32x4*>(tile + ((SHARED ? page_in_step : p) * T + token) * stride + b) = x;
         };
-        if (record) {
-            const Pool& pool = values ? a.v : a.k;
-            bool ok;
-            if (values ? a.tab_lds_v : a.tab_lds_k)
-                ok = rebuild_page<NV>(st, pool, page_tab(pool, smem + (values && !a.same_tab ? a.tab_words_k : 0u)),
-                                      stage, sink);
-            else
-                ok = rebuild_page<NV>(st, pool, page_tab_global(pool), stage, sink);
-            if (!ok) latch_error(pool.err, kErrCorrupt);
-        } else {
+        lds_order();
 #pragma unroll
-            for (int r = 0; r < NV; ++r) sink(256u * r + 4u * lane, st[r]);
+        for (int p = 0; p < PW; ++p) {
+            if ((records >> p) & 1u) {
+                stage_page<NV>(st + p * NV, stage + p * (S::stage_bytes / 4));
+            } else {
+                const uint32_t n = values ? keep[p] : (uint32_t)T;
+#pragma unroll
+                for (int r = 0; r < NV; ++r) row_of(p, n, 256u * r + 4u * lane, st[p * NV + r]);
+            }
         }
+        const Pool& pool = values ? a.v : a.k;
+        const PageTab tab = page_tab(pool, smem + (values && !a.same_tab ? a.tab_words_k : 0u),
+                                     values ? a.tab_lds_v : a.tab_lds_k);
+        for (; records; records &= records - 1) {
+            const uint32_t p = PW == 1 ? 0u : (uint32_t)__builtin_ctz(records);
+            const uint32_t n = !values ? (uint32_t)T : PW == 1 || p == 0 ? keep[0] : keep[PW - 1];
+            if (!rebuild_page<NV>(pool, tab, stage + p * (S::stage_bytes / 4),
+                                  [&](uint32_t w, u32x4 x) __attribute__((always_inline)) { row_of(p, n, w, x); }))
+                latch_error(args_again()->k.err, kErrCorrupt);
+        }
+        lds_order();
     };
 
     // --- the rows' queries (B operand) and running state
     V8 qf[MR][DK];
     float m[MR], l[MR];
     f32x4 o[MR][DN];
-    uint64_t q_row[MR];
-    bool q_on[MR];
+    uint32_t q_row[MR];  // of lane's column; kNoPage past the last row
+    auto row_head = [&](uint32_t rho, uint32_t* j) __attribute__((always_inline)) {
+        const uint32_t i = rho / a.group;
+        *j = rho - i * a.group;
+        return first_row + i;
+    };
+    {
+        const ArgsPtr c = args_again();
 #pragma unroll
-    for (int t = 0; t < MR; ++t) {
-        const uint32_t rho = row0 + 16 * t + col;
-        q_on[t] = rho < rows;
-        const uint32_t i = rho / a.group, j = rho - i * a.group;
-        q_row[t] = first_row + (q_on[t] ? i : 0u);
-        const uint16_t* qp = a.q + (int64_t)q_row[t] * a.q_row + (int64_t)(h * a.group + j) * a.q_head;
+        for (int t = 0; t < MR; ++t) {
+            const uint32_t rho = row0 + 16 * t + col;
+            uint32_t j;
+            q_row[t] = row_head(rho, &j);
+            if (rho >= rows) q_row[t] = kNoPage;
+            const uint16_t* qp = c->q + (int64_t)q_row[t] * c->q_row + (int64_t)(h * a.group + j) * c->q_head;
 #pragma unroll
-        for (int kk = 0; kk < DK; ++kk) {
-            u32x4 x = q_on[t] ? load_eight(qp + 32 * kk + 8 * g, a.q_vec != 0) : u32x4{0u, 0u, 0u, 0u};
-            qf[t][kk] = bits_as<V8>(x ^ a.q_sign);  // (a negative scale is taken into the queries)
+            for (int kk = 0; kk < DK; ++kk) {
+                u32x4 x = {0u, 0u, 0u, 0u};
+                if (rho < rows) x = load_eight(qp + 32 * kk + 8 * g);
+                qf[t][kk] = bits_as<V8>(x ^ c->q_sign);  // (a negative scale is taken into the queries)
+            }
+            m[t] = -__builtin_inff();
+            l[t] = 0.f;
+#pragma unroll
+            for (int n = 0; n < DN; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-        m[t] = -__builtin_inff();
-        l[t] = 0.f;
-#pragma unroll
-        for (int n = 0; n < DN; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-
-    u32x4 st_a[PW * NV], st_b[S::BOTH && !S::ONE ? PW * NV : 1];
-    if (n_steps) {
-        refill(0);
-        load(st_a, 0, only_v, id_a);
-        if (S::BOTH && !S::ONE) load(st_b, 0, true, id_b);
-    }
+    if (n_steps) refill(0);
     // tables of the record formats
     if (4 * threadIdx.x < a.tab_words_k) reinterpret_cast<u32x4*>(smem)[threadIdx.x] = tab_k;
     if (4 * threadIdx.x < a.tab_words_v) reinterpret_cast<u32x4*>(smem + a.tab_words_k)[threadIdx.x] = tab_v;
-    if (a.tab_words_k) stage_page_tables(a.k, smem, kWave * kAttnWaves);
-    if (a.tab_words_v) stage_page_tables(a.v, smem + a.tab_words_k, kWave * kAttnWaves);
-    __syncthreads();
-    for (uint32_t i = 0; i < n_steps; ++i) {
-        const uint32_t s = s_first + i * kStride;
-        const bool draft = TREE && s >= ctx_steps;
-        // tokens held by each page that this wave loads, and what is a record
-        uint32_t n_held[PW], c_held[PW];
+    if (a.tab_words_k > 4 * kWave * kAttnWaves) stage_page_tables(a.k, smem, kWave * kAttnWaves);
+    if (a.tab_words_v > 4 * kWave * kAttnWaves) stage_page_tables(a.v, smem + a.tab_words_k, kWave * kAttnWaves);
+    if (!SHARED) __syncthreads();
+
+    // Iteration i works on step i - 1 and sends for step i, so that each load
+    // stands in the code once.
+    u32x4 st_a[PW * NV], st_b[S::BOTH && !S::ONE ? PW * NV : 1];
+    bool odd = false;
+    uint32_t n_held[PW], records = 0;  // of step i - 1: tokens of each page; which pages are records (keys, then values)
+    uint32_t ids_b = 0;                // the value pages of step i - 1 (ONE)
 #pragma unroll
-        for (int p = 0; p < PW; ++p) {
-            const int at = (int)((i % (64 / PW)) * PW + p);
-            n_held[p] = lane_value(held, at);
-            c_held[p] = lane_value(comp, at);
-            if (draft) {
-                const uint32_t j0 = (s - ctx_steps) * STEP + (SHARED ? page_in_step : (uint32_t)p) * T;
-                n_held[p] = n_new > j0 ? min(n_new - j0, (uint32_t)T) : 0u;
-                c_held[p] = 0;
-            }
-        }
-        auto process = [&](const u32x4* st, bool values, uint32_t bit, char* tile, int stride) __attribute__((
-                           always_inline)) {
-            lds_order();
-#pragma unroll
-            for (int p = 0; p < PW; ++p)
-                put(st + p * NV, p, values, ((c_held[p] >> bit) & 1u) != 0, n_held[p], tile, stride);
-            lds_order();
+    for (int p = 0; p < PW; ++p) n_held[p] = 0;
+    for (uint32_t i = 0; i <= n_steps; ++i) {
+        const bool work = i > 0, more = i < n_steps;
+        const uint32_t s = s_first + (i - 1) * kStride;
+        const bool draft = TREE && work && s >= ctx_steps;
+        auto put_keys = [&]() __attribute__((always_inline)) {
+            put(st_a, false, records & ((1u << PW) - 1), n_held, k_tile, S::RK);
         };
-        const bool more = i + 1 < n_steps;
-        const uint32_t this_b = id_b;
-        uint32_t next_b = kNoPage;
-        auto advance = [&]() __attribute__((always_inline)) {
-            if (more && (i + 1) % (64 / PW) == 0) refill(i + 1);
-            next_b = id_b;
+        auto put_values = [&](u32x4* st, uint32_t shift) __attribute__((always_inline)) {
+            // Infinities and NaNs of drafted values are taken out, so that
+            // they reach no row through a product with a weight of zero, and
+            // added at the end to the rows that see them.
+            if (draft) {
+#pragma unroll
+                for (int r = 0; r < PW * NV; ++r) odd |= clear_odd<E>(st[r]);
+            }
+            put(st, true, records >> shift, n_held, v_tile, S::RV);
         };
         if constexpr (SHARED) {
-            __syncthreads();  // the tiles are free
-            if (S::BOTH) {
-                process(st_a, false, 0, k_tile, S::RK);
-                process(st_b, true, 1, v_tile, S::RV);
-            } else if (only_v) {
-                process(st_a, true, 0, v_tile, S::RV);
-            } else {
-                process(st_a, false, 0, k_tile, S::RK);
+            __syncthreads();  // the tiles are free (and the tables there)
+            if (work) {
+                if (S::BOTH) {
+                    put_keys();
+                    put_values(st_b, PW);
+                } else if (only_v) {
+                    put_values(st_a, 0);
+                } else {
+                    put_keys();
+                }
             }
-            advance();
-            if (more) {
-                load(st_a, i + 1, only_v, id_a);
-                if (S::BOTH) load(st_b, i + 1, true, next_b);
-            }
-            __syncthreads();
         } else {
-            process(st_a, false, 0, k_tile, S::RK);
-            if constexpr (S::ONE) {
-                load(st_a, i, true, this_b);
-                advance();
-            } else {
-                advance();
-                if (more) load(st_a, i + 1, false, id_a);
-            }
+            if (work) put_keys();
         }
-
+        const uint32_t step_held_all =
+            draft ? min(n_new - (s - ctx_steps) * STEP, (uint32_t)STEP) : min((uint32_t)len - s * STEP, (uint32_t)STEP);
+        uint32_t tiles_held[!TREE && !SHARED ? PW : 1];  // tokens of the pages of step i - 1, for the masks
+        if constexpr (!TREE && !SHARED) {
+#pragma unroll
+            for (int p = 0; p < PW; ++p) tiles_held[p] = n_held[p];
+        }
+        // step i: its pages' facts (once step i - 1's values have been put),
+        // and its loads
+        uint32_t next_held[PW], next_records = 0;
+        const uint32_t this_b = ids_b;
+        if (more) {
+            if (i > 0 && i % (64 / PW) == 0) refill(i);
+            const uint32_t sn = s_first + i * kStride;
+#pragma unroll
+            for (int p = 0; p < PW; ++p) {
+                const int at = (int)((i % (64 / PW)) * PW + p);
+                next_held[p] = lane_value(held, at);
+                const uint32_t c = lane_value(comp, at);
+                next_records |= (c & 1u) << p | (c >> 1) << (PW + p);
+                if (TREE && sn >= ctx_steps) {
+                    const uint32_t j0 = (sn - ctx_steps) * STEP + (SHARED ? page_in_step : (uint32_t)p) * T;
+                    next_held[p] = n_new > j0 ? min(n_new - j0, (uint32_t)T) : 0u;
+                }
+            }
+            if constexpr (!S::ONE) load(st_a, i, only_v, id_a);
+            if constexpr (SHARED && S::BOTH) load(st_b, i, true, id_b);
+        }
+        if constexpr (S::ONE) {
+            if (work) load(st_a, i - 1, true, this_b);
+        }
+        auto advance = [&]() __attribute__((always_inline)) {
+            records = next_records;
+            ids_b = id_b;
+#pragma unroll
+            for (int p = 0; p < PW; ++p) n_held[p] = next_held[p];
+        };
+        if constexpr (SHARED) {
+            __syncthreads();
+            if (more) advance();
+        }
+        if (!work) {
+            if constexpr (!SHARED) {
+                if (more) {
+                    if constexpr (S::ONE)
+                        load(st_a, i, false, id_a);
+                    else
+                        load(st_b, i, true, id_b);
+                    advance();
+                }
+            }
+            continue;
+        }
 #pragma unroll 1
         for (uint32_t c = 0; c < (uint32_t)(STEP / S::CHUNK); ++c) {
-        // valid tokens of each tile of 16
-        const uint32_t t0 = c * S::CHUNK;
-        uint32_t step_held = 0;
-        if (SHARED || TREE) {
-            const int64_t n = draft ? (int64_t)n_new - (int64_t)(s - ctx_steps) * STEP : len - (int64_t)s * STEP;
-            step_held = (uint32_t)max(min(n, (int64_t)STEP) - (int64_t)t0, (int64_t)0);
-        }
-        auto tile_held = [&](int u) __attribute__((always_inline)) -> uint32_t {
-            if constexpr (TREE || SHARED) {
-                return step_held > 16u * u ? step_held - 16u * u : 0u;
-            } else {
-                const uint32_t n = n_held[(u * 16) / T < PW ? (u * 16) / T : 0];
-                return n > (uint32_t)(u * 16 % T) ? n - (uint32_t)(u * 16 % T) : 0u;
-            }
-        };
-
-        const char* const kt = k_tile + t0 * S::RK;
-        const char* const vt = v_tile + t0 * S::RV;
-        // S^T = K Q^T
-        f32x4 sc[MR][TILES];
-#pragma unroll
-        for (int u = 0; u < TILES; ++u) {
-#pragma unroll
-            for (int t = 0; t < MR; ++t) sc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int kk = 0; kk < DK; ++kk) {
-                const V8 kf =
-                    *reinterpret_cast<const V8*>(kt + (16 * u + col) * S::RK + 64 * kk + 16 * g);
-#pragma unroll
-                for (int t = 0; t < MR; ++t) sc[t][u] = E::mfma(kf, qf[t][kk], sc[t][u]);
-            }
-        }
-        // masked scores -infinity, the running maximum, weights
-        bool whole = !draft;
-#pragma unroll
-        for (int u = 0; u < TILES; ++u) whole = whole && tile_held(u) >= 16u;
-#pragma unroll
-        for (int t = 0; t < MR; ++t) {
-            uint32_t seen[(TILES + 1) / 2];
-            if (draft) {
-#pragma unroll
-                for (int w = 0; w < (TILES + 1) / 2; ++w) {
-                    const uint32_t word = (s - ctx_steps) * (STEP / 32) + t0 / 32 + w;
-                    seen[w] = q_on[t] && word < a.mask_words2 ? a.mask[q_row[t] * a.mask_words2 + word] : 0u;
+            // valid tokens of each tile of 16
+            const uint32_t t0 = c * S::CHUNK;
+            auto tile_held = [&](int u) __attribute__((always_inline)) -> uint32_t {
+                if constexpr (TREE || SHARED) {
+                    const uint32_t before = t0 + 16u * u;
+                    return step_held_all > before ? step_held_all - before : 0u;
+                } else {
+                    const uint32_t n = tiles_held[(u * 16) / T < PW ? (u * 16) / T : 0];
+                    return n > (uint32_t)(u * 16 % T) ? n - (uint32_t)(u * 16 % T) : 0u;
                 }
-            }
-            float top = -__builtin_inff();
+            };
+            const char* const kt = k_tile + t0 * S::RK;
+            const char* const vt = v_tile + t0 * S::RV;
+            // S^T = K Q^T
+            f32x4 sc[MR][TILES];
 #pragma unroll
             for (int u = 0; u < TILES; ++u) {
-                if (!whole) {
-                    const uint32_t n = tile_held(u);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        bool on = 4 * g + e < n;
-                        if (draft) on = on && ((seen[u >> 1] >> (16 * (u & 1) + 4 * g + e)) & 1u);
-                        sc[t][u][e] = on ? sc[t][u][e] : -__builtin_inff();
+                for (int t = 0; t < MR; ++t) sc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kk = 0; kk < DK; ++kk) {
+                    const V8 kf = *reinterpret_cast<const V8*>(kt + (16 * u + col) * S::RK + 64 * kk + 16 * g);
+#pragma unroll
+                    for (int t = 0; t < MR; ++t) sc[t][u] = E::mfma(kf, qf[t][kk], sc[t][u]);
+                }
+            }
+            // masked scores -infinity, the running maximum, weights
+            bool whole = !draft;
+#pragma unroll
+            for (int u = 0; u < TILES; ++u) whole = whole && tile_held(u) >= 16u;
+            if (!whole) {
+                const ArgsPtr x = args_again();
+#pragma unroll
+                for (int t = 0; t < MR; ++t) {
+#pragma unroll
+                    for (int u = 0; u < TILES; ++u) {
+                        // bit j of `seen`: the lane's row sees token j of the tile
+                        uint32_t seen = tile_held(u) >= 16u ? 0xFFFFu : (1u << tile_held(u)) - 1u;
+                        if (draft) {
+                            const uint32_t word = (s - ctx_steps) * (STEP / 32) + t0 / 32 + u / 2;
+                            uint32_t bits = 0;
+                            if (q_row[t] != kNoPage && word < x->mask_words2)
+                                bits = x->mask[(uint64_t)q_row[t] * x->mask_words2 + word];
+                            seen &= bits >> (16 * (u & 1));
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sc[t][u][e] = (seen >> (4 * g + e)) & 1u ? sc[t][u][e] : -__builtin_inff();
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[t][u][e]);
             }
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            top *= a.scale2;
-            // The maximum is moved only when a score passes it by more than
-            // 8 (weights then stay below 2^8 and sums far from overflow), so
-            // most steps rescale nothing.
-            if (ballot(top > m[t] + 8.f || (m[t] == -__builtin_inff() && top != -__builtin_inff()))) {
-                const float m_new = fmaxf(m[t], top);
-                const float f = m_new == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(m[t] - m_new);
-                m[t] = m_new;
-                l[t] *= f;
 #pragma unroll
-                for (int n = 0; n < DN; ++n) o[t][n] *= f;
-            }
-            const float base = m[t] == -__builtin_inff() ? 0.f : -m[t];
+            for (int t = 0; t < MR; ++t) {
+                float top = -__builtin_inff();
 #pragma unroll
-            for (int u = 0; u < TILES; ++u) {
+                for (int u = 0; u < TILES; ++u) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][u][e], a.scale2, base));
-                    sc[t][u][e] = p;
-                    l[t] += p;
+                    for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[t][u][e]);
+                }
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                top *= a.scale2;
+                // The maximum is moved only when a score passes it by more
+                // than 8 (weights then stay below 2^8 and sums far from
+                // overflow), so most steps rescale nothing.
+                if (ballot(top > m[t] + 8.f || (m[t] == -__builtin_inff() && top != -__builtin_inff()))) {
+                    const float m_new = fmaxf(m[t], top);
+                    const float f = m_new == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(m[t] - m_new);
+                    m[t] = m_new;
+                    l[t] *= f;
+#pragma unroll
+                    for (int n = 0; n < DN; ++n) o[t][n] *= f;
+                }
+                const float base = m[t] == -__builtin_inff() ? 0.f : -m[t];
+#pragma unroll
+                for (int u = 0; u < TILES; ++u) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][u][e], a.scale2, base));
+                        sc[t][u][e] = p;
+                        l[t] += p;
+                    }
                 }
             }
-        }
 
-        // O^T += V^T P^T
-        if constexpr (S::ONE) {
-            process(st_a, true, 1, v_tile, S::RV);
-            if (more) load(st_a, i + 1, false, id_a);
-        } else if constexpr (!SHARED) {
-            process(st_b, true, 1, v_tile, S::RV);
-            if (more) load(st_b, i + 1, true, next_b);
-        }
-        {
+            if constexpr (!SHARED) put_values(S::ONE ? st_a : st_b, PW);
+            if constexpr (!SHARED) {
+                if (more) {
+                    if constexpr (S::ONE)
+                        load(st_a, i, false, id_a);
+                    else
+                        load(st_b, i, true, id_b);
+                    advance();
+                }
+            }
+            // O^T += V^T P^T
 #pragma unroll
             for (int u = 0; u < TILES; u += 2) {
                 V8 pf[MR];
@@ -478,27 +532,27 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
                     for (int t = 0; t < MR; ++t) o[t][n] = E::mfma(vf, pf[t], o[t][n]);
                 }
             }
-        }
-        lds_order();
+            lds_order();
         }
     }
 
     // --- the sums over the four lanes of a row, then the result or this split's part
-    const uint32_t nq = a.kv_heads * a.group;
-    auto finish = [&](uint64_t row, uint32_t head, uint32_t d, f32x4 x, float mm, float ll) __attribute__((
+    const ArgsPtr c = args_again();
+    const uint32_t nq = c->kv_heads * c->group, splits = c->splits;
+    auto finish = [&](uint32_t row, uint32_t head, uint32_t d, f32x4 x, float mm, float ll) __attribute__((
                       always_inline)) {
-        const uint64_t rh = row * nq + head;
-        if (a.splits == 1) {
+        const uint64_t rh = (uint64_t)row * nq + head;
+        if (splits == 1) {
             const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
             const u32x2 y = {E::pack(x[0] * inv, x[1] * inv), E::pack(x[2] * inv, x[3] * inv)};
-            *reinterpret_cast<u32x2*>(a.out + rh * D + d) = y;
-            if (d == 0 && a.lse)
-                a.lse[rh] = ll > 0.f || ll != ll ? (mm + __builtin_amdgcn_logf(ll)) * kLn2 : -__builtin_inff();
+            *reinterpret_cast<u32x2*>(c->out + rh * D + d) = y;
+            if (d == 0 && c->lse)
+                c->lse[rh] = ll > 0.f || ll != ll ? (mm + __builtin_amdgcn_logf(ll)) * kLn2 : -__builtin_inff();
         } else {
-            *reinterpret_cast<f32x4*>(a.part + (rh * a.splits + split) * D + d) = x;
+            *reinterpret_cast<f32x4*>(c->part + (rh * splits + split) * D + d) = x;
             if (d == 0) {
-                a.part_ml[(rh * a.splits + split) * 2] = mm;
-                a.part_ml[(rh * a.splits + split) * 2 + 1] = ll;
+                c->part_ml[(rh * splits + split) * 2] = mm;
+                c->part_ml[(rh * splits + split) * 2 + 1] = ll;
             }
         }
     };
@@ -507,10 +561,11 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
         l[t] += __shfl_xor(l[t], 16);
         l[t] += __shfl_xor(l[t], 32);
         if constexpr (SHARED) {
-            if (q_on[t]) {
-                const uint32_t rho = row0 + 16 * t + col, j = rho % a.group;
+            uint32_t j;
+            const uint32_t row = row_head(row0 + 16 * t + col, &j);
+            if (q_row[t] != kNoPage) {
 #pragma unroll
-                for (int n = 0; n < DN; ++n) finish(q_row[t], h * a.group + j, 16 * n + 4 * g, o[t][n], m[t], l[t]);
+                for (int n = 0; n < DN; ++n) finish(row, h * a.group + j, 16 * n + 4 * g, o[t][n], m[t], l[t]);
             }
         } else {
             // the waves' rows joined through LDS: [wave][row][D + 4]
@@ -524,23 +579,25 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
                 join_l[wib][col] = l[t];
             }
             __syncthreads();
+#pragma unroll 1
             for (uint32_t e = threadIdx.x; e < 16 * (D / 4); e += kWave * kAttnWaves) {
-                const uint32_t c = e / (D / 4), d = 4 * (e % (D / 4));
-                const uint32_t rho = row0 + 16 * t + c;
-                if (rho >= rows) continue;
+                const uint32_t cc = e / (D / 4), d = 4 * (e % (D / 4));
+                const uint32_t rho = row0 + 16 * t + cc;
+                if (rho >= rows) break;
                 float mm = -__builtin_inff(), ll = 0.f;
 #pragma unroll
-                for (uint32_t w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, join_m[w][c]);
+                for (uint32_t w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, join_m[w][cc]);
                 const float base = mm == -__builtin_inff() ? 0.f : mm;
                 f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (uint32_t w = 0; w < kAttnWaves; ++w) {
-                    const float f = __builtin_amdgcn_exp2f(join_m[w][c] - base);
-                    ll += f * join_l[w][c];
-                    x += f * *reinterpret_cast<const f32x4*>(buf + (w * 16 + c) * (D + 4) + d);
+                    const float f = __builtin_amdgcn_exp2f(join_m[w][cc] - base);
+                    ll += f * join_l[w][cc];
+                    x += f * *reinterpret_cast<const f32x4*>(buf + (w * 16 + cc) * (D + 4) + d);
                 }
-                const uint32_t i = rho / a.group, j = rho - i * a.group;
-                finish(first_row + i, h * a.group + j, d, x, mm, ll);
+                uint32_t j;
+                const uint32_t row = row_head(rho, &j);
+                finish(row, h * a.group + j, d, x, mm, ll);
             }
         }
     }
@@ -554,24 +611,24 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
             const uint32_t j_hi = s_hi > ctx_steps ? min((s_hi - ctx_steps) * STEP, n_new) : 0u;
             const uint32_t n_rows = min(rows - rt * kRowsWg, kRowsWg);
             for (uint32_t e = threadIdx.x; e < n_rows * D; e += kWave * kAttnWaves) {
-                const uint32_t rho = rt * kRowsWg + e / D, d = e % D;
-                const uint32_t i = rho / a.group, j = rho - i * a.group;
-                const uint64_t row = first_row + i;
+                const uint32_t d = e % D;
+                uint32_t j;
+                const uint32_t row = row_head(rt * kRowsWg + e / D, &j);
                 float sum = 0.f;
                 bool any = false;
                 for (uint32_t k = j_lo; k < j_hi; ++k) {
-                    if (!((a.mask[row * a.mask_words2 + k / 32] >> (k % 32)) & 1u)) continue;
-                    const uint32_t v = a.v_new[(int64_t)(first_row + k) * a.new_row + (int64_t)h * a.new_head + d];
+                    if (!((c->mask[(uint64_t)row * c->mask_words2 + k / 32] >> (k % 32)) & 1u)) continue;
+                    const uint32_t v = c->v_new[(int64_t)(first_row + k) * c->new_row + (int64_t)h * c->new_head + d];
                     if ((v & E::kExponent) != E::kExponent) continue;
                     sum += E::from_bits(v);
                     any = true;
                 }
                 if (!any) continue;
-                const uint64_t rh = row * nq + h * a.group + j;
-                if (a.splits == 1)
-                    a.out[rh * D + d] = (uint16_t)E::pack(E::from_bits(a.out[rh * D + d]) + sum, 0.f);
+                const uint64_t rh = (uint64_t)row * nq + h * a.group + j;
+                if (splits == 1)
+                    c->out[rh * D + d] = (uint16_t)E::pack(E::from_bits(c->out[rh * D + d]) + sum, 0.f);
                 else
-                    a.part[(rh * a.splits + split) * D + d] += sum;
+                    c->part[(rh * splits + split) * D + d] += sum;
             }
         }
     }

@@ -15,14 +15,15 @@ constexpr uint32_t kNoPage = 0xFFFFFFFFu;
 constexpr uint64_t kMaxPoolSlots = 0xFFFFFFFEull;  // page ids are held in 32 bits
 constexpr uint64_t kMaxPageBytes = 4ull * kMaxTileWords;
 
-// A pool of pages as a kernel sees it.  The tables are those of the handle;
-// a position of the period holds Mask/Bitval's word and what the rebuild
-// needs of it (Tables).
+// A pool of pages as a kernel sees it.  `tab` is row kd of the handle's
+// tables: in device memory row b (Bitval) lies one row before it, the dx rows
+// from one row and the r rows from five rows behind it, all src_Mw words
+// apart.
 struct Pool {
     const uint8_t* slots;
     const uint32_t* bitmask;
     uint32_t* err;
-    Tables t;
+    const uint32_t* tab;
     uint32_t n_slots;
     uint32_t Mw;      // period in words; 1 where every position has the same Mask/Bitval word
     uint32_t src_Mw;  // words between the rows of the tables in device memory
@@ -32,14 +33,16 @@ struct Pool {
     uint32_t valid;   // participation bits of the last header word
 };
 
-// Per-position tables as the rebuild reads them: rows kd, b, dx (one per four
-// runs past the third), r (one per run), each `stride` words.
+// Rows of a table as the rebuild reads them, all `stride` words: kd, b, dx
+// (one per four runs past the third), r (one per run) in LDS; in device
+// memory (in_lds 0) as above.  Pointers to LDS keep their address space: a
+// choice between two generic pointers would be read with flat loads.
+typedef const __attribute__((address_space(3))) uint32_t* LdsWords;
+typedef const __attribute__((address_space(3))) u32x4* LdsVectors;
 struct PageTab {
-    const uint32_t* kd;
-    const uint32_t* b;
-    const uint32_t* dx;
-    const uint32_t* r;
-    uint32_t stride, runs;
+    LdsWords lds;
+    const uint32_t* mem;
+    uint32_t in_lds, stride, runs;
 };
 
 __host__ __device__ constexpr uint32_t page_dx_rows(uint32_t runs) { return runs > 3 ? runs / 4u : 0u; }
@@ -50,14 +53,15 @@ __host__ __device__ constexpr uint32_t page_tab_words(uint32_t Mw, uint32_t runs
     return (2u + page_dx_rows(runs) + runs) * page_tab_stride(Mw);
 }
 
+__device__ __forceinline__ int32_t page_tab_source_row(uint32_t row, uint32_t dxr) {
+    return row == 0 ? 0 : row == 1 ? -1 : row < 2 + dxr ? (int32_t)row - 1 : (int32_t)(row - 2 - dxr) + 5;
+}
+
 // Vector i (four words) of the pool's tables as they stand in LDS.
 __device__ __forceinline__ u32x4 page_table_vector(const Pool& p, uint32_t i) {
     const uint32_t S = page_tab_stride(p.Mw), dxr = page_dx_rows(p.runs);
     const uint32_t row = (4 * i) >> (31 - __builtin_clz(S)), pos = (4 * i) & (S - 1);  // periods are powers of two
-    const uint32_t* src = row == 0 ? p.t.kd
-                          : row == 1 ? p.t.b
-                          : row < 2 + dxr ? p.t.dx + (row - 2) * p.src_Mw
-                                          : p.t.r + (row - 2 - dxr) * p.src_Mw;
+    const uint32_t* src = p.tab + (int64_t)page_tab_source_row(row, dxr) * p.src_Mw;
     if (p.Mw >= 4) return *reinterpret_cast<const u32x4*>(src + pos);
     const uint32_t x = src[0], y = src[p.Mw - 1];
     return u32x4{x, y, x, y};
@@ -77,13 +81,16 @@ __device__ __forceinline__ void stage_page_tables(const Pool& p, uint32_t* lds, 
     }
 }
 
-__device__ __forceinline__ PageTab page_tab(const Pool& p, const uint32_t* lds) {
-    const uint32_t S = page_tab_stride(p.Mw), dxr = page_dx_rows(p.runs);
-    return PageTab{lds, lds + S, lds + 2 * S, lds + (2 + dxr) * S, S, p.runs};
+// The tables at `lds`, or where they lie in device memory (in_lds 0; a period
+// of at least four words).
+__device__ __forceinline__ PageTab page_tab(const Pool& p, const uint32_t* lds, uint32_t in_lds) {
+    return PageTab{(LdsWords)lds, p.tab, in_lds, in_lds ? page_tab_stride(p.Mw) : p.src_Mw, p.runs};
 }
-// The tables where they lie in device memory (period of at least four words).
-__device__ __forceinline__ PageTab page_tab_global(const Pool& p) {
-    return PageTab{p.t.kd, p.t.b, p.t.dx, p.t.r, p.Mw, p.runs};
+
+// Four positions of a row: at `lds_row` in LDS, `mem_row` in device memory.
+__device__ __forceinline__ u32x4 tab_vector(const PageTab& t, uint32_t lds_row, int32_t mem_row, uint32_t pos) {
+    if (t.in_lds) return *(LdsVectors)(t.lds + lds_row * t.stride + pos);
+    return *reinterpret_cast<const u32x4*>(t.mem + (int64_t)mem_row * t.stride + pos);
 }
 
 // LDS words that one wave needs to rebuild a page of NV vectors per lane: the
@@ -94,36 +101,47 @@ __host__ __device__ constexpr uint32_t page_stage_words() {
     return 256u * NV + (256u * NV / 32u) + 8u;
 }
 
-// One wave.  st[r] of lane l: words 256 r + 4 l .. + 3 of a slot that holds a
-// record; sink(w, x) receives words w .. w + 3 of the page, w = 256 s + 4 l
-// for s = 0 .. NV - 1.  stage: page_stage_words<NV> words of this wave's LDS.
-// Returns false for a record that is not valid (header padding set, or as
-// long as the page).
+// One wave: a slot from registers (load_page) to its LDS.
+template <int NV>
+__device__ __forceinline__ void stage_page(const u32x4* st, uint32_t* stage) {
+    const uint32_t lane = lane_id();
+#pragma unroll
+    for (int r = 0; r < NV; ++r) reinterpret_cast<u32x4*>(stage)[r * kWave + lane] = st[r];
+    if (lane < 8) stage[256 * NV + lane] = 0;
+}
+
+// One wave: the record in stage (page_stage_words<NV> words of this wave's
+// LDS) rebuilt; sink(w, x) receives words w .. w + 3 of the page, w = 256 s +
+// 4 l for s = 0 .. NV - 1.  Returns false for a record that is not valid
+// (header padding set, or as long as the page).
 //
 // The rebuild is the codec's: a lane's four words take p ? 32 - k : 32 bits
 // each, a wave scan gives their start bits, a funnel shift cuts the field out
 // of two words of the record, and the field's runs go to their places.  The
 // loop over s is not unrolled: unrolled, its table and record reads were
-// hoisted together and the attention kernels spilled registers.
+// hoisted together and the attention kernels spilled registers.  With a
+// period of at most 256 words (one step) a lane's positions are the same in
+// every step, and its table entries are read once.
 template <int NV, class Sink>
-__device__ __forceinline__ bool rebuild_page(const u32x4* st, const Pool& p, const PageTab& tab, uint32_t* stage,
-                                             Sink sink) {
+__device__ __forceinline__ bool rebuild_page(const Pool& p, const PageTab& tab, const uint32_t* stage, Sink sink) {
     const uint32_t lane = lane_id();
     __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int r = 0; r < NV; ++r) reinterpret_cast<u32x4*>(stage)[r * kWave + lane] = st[r];
-    if (lane < 8) stage[256 * NV + lane] = 0;
-    __builtin_amdgcn_wave_barrier();
     const uint32_t* pay = stage + p.hw;
-    const uint32_t lg = p.log2g;
+    const uint32_t lg = p.log2g, runs = tab.runs, dxr = page_dx_rows(runs);
     const bool ok = p.valid >= 32 || (stage[p.hw - 1] >> p.valid) == 0;
     uint32_t carry = 0;
+    u32x4 kd = {0u, 0u, 0u, 0u}, bv = kd, rm[3] = {kd, kd, kd};
 #pragma unroll 1
     for (int s = 0; s < NV; ++s) {
         const uint32_t w0 = 256u * s + 4u * lane;
         const uint32_t pos = w0 & (tab.stride - 1);
-        const u32x4 kd = *reinterpret_cast<const u32x4*>(tab.kd + pos);
-        u32x4 x = *reinterpret_cast<const u32x4*>(tab.b + pos);
+        if (s == 0 || tab.stride > 256u) {
+            kd = tab_vector(tab, 0, 0, pos);
+            bv = tab_vector(tab, 1, -1, pos);
+#pragma unroll
+            for (uint32_t r = 0; r < 3; ++r)
+                if (r < runs) rm[r] = tab_vector(tab, 2 + dxr + r, 5 + r, pos);
+        }
         const uint32_t c0 = w0 >> lg;
         const uint32_t h = stage[c0 >> 5] >> (c0 & 31u);
         uint32_t part[4], size[4], tot = 0;
@@ -143,19 +161,16 @@ __device__ __forceinline__ bool rebuild_page(const u32x4* st, const Pool& p, con
             f[j] = funnel(pay[q + 1], pay[q], off);
             off += size[j];
         }
+        u32x4 x = bv;
 #pragma unroll
-        for (uint32_t r = 0; r < 3; ++r) {
-            if (r < tab.runs) {
-                const u32x4 rm = *reinterpret_cast<const u32x4*>(tab.r + r * tab.stride + pos);
+        for (uint32_t r = 0; r < 3; ++r)  // (rows that are not there stay zero)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] |= (f[j] << ((kd[j] >> (8 * (r + 1))) & 31u)) & rm[j];
-            }
-        }
-        for (uint32_t r = 3; r < tab.runs; ++r) {
-            const u32x4 rm = *reinterpret_cast<const u32x4*>(tab.r + r * tab.stride + pos);
-            const u32x4 dv = *reinterpret_cast<const u32x4*>(tab.dx + ((r - 3) >> 2) * tab.stride + pos);
+            for (int j = 0; j < 4; ++j) x[j] |= (f[j] << ((kd[j] >> (8 * (r + 1))) & 31u)) & rm[r][j];
+        for (uint32_t r = 3; r < runs; ++r) {
+            const u32x4 m = tab_vector(tab, 2 + dxr + r, 5 + r, pos);
+            const u32x4 dv = tab_vector(tab, 2 + ((r - 3) >> 2), 1 + ((r - 3) >> 2), pos);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] |= (f[j] << ((dv[j] >> (8 * ((r - 3) & 3u))) & 31u)) & rm[j];
+            for (int j = 0; j < 4; ++j) x[j] |= (f[j] << ((dv[j] >> (8 * ((r - 3) & 3u))) & 31u)) & m[j];
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = part[j] ? x[j] : f[j];

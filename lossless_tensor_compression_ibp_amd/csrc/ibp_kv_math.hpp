@@ -53,18 +53,11 @@ struct Fp16 {
     static constexpr uint32_t kExponent = 0x7C00u;
 };
 
-// Eight numbers of a dense row; `vec`: it is 16-byte aligned.
-__device__ __forceinline__ u32x4 load_eight(const uint16_t* p, bool vec) {
-    if (vec) return *reinterpret_cast<const u32x4*>(p);
-    u32x4 x;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = (uint32_t)p[2 * j] | ((uint32_t)p[2 * j + 1] << 16);
-    return x;
-}
-
-// Whether rows and heads of a dense tensor all start on 16 bytes.
-inline uint32_t vectors_ok(const void* p, int64_t row, int64_t head) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row % 8 == 0 && head % 8 == 0 ? 1u : 0u;
+// Eight numbers of a dense row, which need not start on more than two bytes
+// (the memory of this GPU takes 16-byte reads at any address).
+__device__ __forceinline__ u32x4 load_eight(const uint16_t* p) {
+    typedef u32x4 u32x4_any __attribute__((aligned(2)));
+    return *reinterpret_cast<const u32x4_any*>(p);
 }
 
 // The pool of k as the kernels see it.
@@ -74,11 +67,14 @@ inline ibp_status make_pool(const ibp_pages* k, int device, Pool* out) {
     if (k->n_slots == 0 || k->n_slots > kMaxPoolSlots) return IBP_ERR_INVALID_ARG;
     if (!device_or_pinned(k->slots, device) || !device_only(k->bitmask, device)) return IBP_ERR_INVALID_ARG;
     if (!aligned16(h->params.tensor_bytes, {k->slots})) return IBP_ERR_UNSUPPORTED;
+    // the tables' rows as Pool describes them
+    if (h->tabs.b != h->tabs.kd - h->Mw || h->tabs.dx != h->tabs.kd + h->Mw || h->tabs.r != h->tabs.kd + 5ull * h->Mw)
+        return IBP_ERR_UNSUPPORTED;
     const uint64_t chunks = 8 * h->params.tensor_bytes / h->params.chunk_bits;
     out->slots = static_cast<const uint8_t*>(k->slots);
     out->bitmask = k->bitmask;
     out->err = h->d_err;
-    out->t = h->tabs;
+    out->tab = h->tabs.kd;
     out->n_slots = (uint32_t)k->n_slots;
     out->Mw = h->sum.uniform ? 1u : h->Mw;
     out->src_Mw = h->Mw;

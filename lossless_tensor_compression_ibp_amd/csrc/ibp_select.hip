@@ -49,7 +49,7 @@ __global__ __launch_bounds__(kWave * kBoundWaves) void k_page_bounds(Pool pool, 
         stage_page_tables(pool, smem);
         __syncthreads();
     }
-    const PageTab tab = TAB_LDS ? page_tab(pool, smem) : page_tab_global(pool);
+    const PageTab tab = page_tab(pool, smem, TAB_LDS);
     uint32_t* stage = smem + tab_words + wib * page_stage_words<NV>();
     const uint32_t row_lanes = row_words / 4;  // lanes that one token takes
     const uint64_t stride = (uint64_t)gridDim.x * kBoundWaves;
@@ -62,6 +62,7 @@ __global__ __launch_bounds__(kWave * kBoundWaves) void k_page_bounds(Pool pool, 
             latch_error(pool.err, kErrRange);
             continue;
         }
+        __builtin_amdgcn_wave_barrier();
         u32x4 st[NV];
         load_page<NV>(st, pool.slots, id);
         float lo[8], hi[8];
@@ -79,7 +80,8 @@ __global__ __launch_bounds__(kWave * kBoundWaves) void k_page_bounds(Pool pool, 
             }
         };
         if (uniform(page_bit(pool.bitmask, id))) {
-            if (!rebuild_page<NV>(st, pool, tab, stage, take)) latch_error(pool.err, kErrCorrupt);
+            stage_page<NV>(st, stage);
+            if (!rebuild_page<NV>(pool, tab, stage, take)) latch_error(pool.err, kErrCorrupt);
         } else {
 #pragma unroll
             for (int r = 0; r < NV; ++r) take(256u * r + 4u * lane, st[r]);
@@ -138,7 +140,6 @@ struct SelectArgs {
     uint32_t wave_rows;      // rows of one wave
     uint32_t span;           // times 64 blocks per wave
     uint32_t same_blocks;    // a workgroup's waves take the same blocks, and rows of their own
-    uint32_t vec;            // q rows may be read as 16-byte vectors
 };
 
 constexpr uint32_t kScoreWaves = 4;
@@ -201,7 +202,7 @@ __global__ __launch_bounds__(kWave * kScoreWaves, 2) void k_scores(SelectArgs a)
                                     (int64_t)(h * a.group + head) * a.q_head;
 #pragma unroll
                 for (int kk = 0; kk < DK; ++kk) {
-                    const u32x4 v = on ? load_eight(q + 32 * kk + 8 * g, a.vec != 0) : u32x4{0u, 0u, 0u, 0u};
+                    const u32x4 v = on ? load_eight(q + 32 * kk + 8 * g) : u32x4{0u, 0u, 0u, 0u};
                     u32x4 p, m;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -477,7 +478,7 @@ __device__ __forceinline__ uint32_t exact_key(const SelectArgs& a, uint64_t r, u
 #pragma unroll
         for (int d = 0; d < D; d += 128) {
             if (d + 8 * part < (uint32_t)D) {
-                const u32x4 x = load_eight(q + d + 8 * part, a.vec != 0);
+                const u32x4 x = load_eight(q + d + 8 * part);
                 const u32x4 lo = *reinterpret_cast<const u32x4*>(bounds + d + 8 * part);
                 const u32x4 hi = *reinterpret_cast<const u32x4*>(bounds + D + d + 8 * part);
 #pragma unroll
@@ -811,7 +812,6 @@ ibp_status ibp_select_pages(ibp_meta_t h, const ibp_attention* a, const void* q,
     s.log2_pad = s.pad > 16 ? 31 : (uint32_t)__builtin_ctz(s.pad);
     s.rows_per_tile = s.pad < 16 ? 16 / s.pad : 1;
     s.head_tiles = s.pad > 16 ? s.pad / 16 : 1;
-    s.vec = vectors_ok(q, a->q_row_stride, a->q_head_stride);
     // Many rows per sequence share the pages' bounds, two tiles of rows a wave
     // (one of 256 dims, for the registers); few rows take a wave each.
     const bool shared = a->n_rows >= 4 * a->n_seqs && s.head_tiles == 1;
