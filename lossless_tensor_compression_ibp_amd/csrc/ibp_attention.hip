@@ -26,7 +26,8 @@ void shape_of(AttnPlan* p) {
 
 // Rows per workgroup, split of the context, LDS.  `rows`: most rows of one
 // (sequence or row, key/value head).
-AttnPlan plan_attention(const ibp_attention* a, bool tree, uint64_t items, uint64_t rows, uint64_t tokens) {
+AttnPlan plan_attention(const ibp_attention* a, bool tree, uint64_t items, uint64_t rows, uint64_t tokens,
+                        uint64_t new_tokens) {
     AttnPlan p;
     const uint32_t D = a->head_dim, T = a->page_tokens;
     const uint32_t m2 = D <= 128 ? 2 : 1;
@@ -48,10 +49,10 @@ AttnPlan plan_attention(const ibp_attention* a, bool tree, uint64_t items, uint6
     IBP_SHAPE(128, 32)
     IBP_SHAPE(256, 16)
 #undef IBP_SHAPE
-    const uint64_t steps = (tokens + p.step - 1) / p.step;
+    const uint64_t steps = (tokens + p.step - 1) / p.step + (new_tokens + p.step - 1) / p.step;
     const uint64_t groups = items * a->n_kv_heads * p.row_tiles;
-    const uint64_t least = p.shared ? 2 : 2 * kAttnWaves;  // steps that make a split worth joining
-    const uint64_t most = std::max<uint64_t>(1, steps / least);
+    const uint64_t least = p.shared ? 2 : kAttnWaves;  // steps that make a split worth joining
+    const uint64_t most = std::max<uint64_t>(1, (steps + least - 1) / least);
     p.splits = (uint32_t)std::min({most, (kTargetGroups + groups - 1) / groups, kMaxSplits});
     return p;
 }
@@ -67,11 +68,11 @@ uint64_t context_hint(const ibp_attention* a) {
 
 AttnPlan plan_tree(const ibp_attention* a) {
     return plan_attention(a, true, a->n_seqs, (uint64_t)a->max_new * (a->n_q_heads / a->n_kv_heads),
-                          context_hint(a) + a->max_new);
+                          context_hint(a), a->max_new);
 }
 
 AttnPlan plan_sparse(const ibp_attention* a, uint32_t n_blocks) {
-    return plan_attention(a, false, a->n_rows, a->n_q_heads / a->n_kv_heads, (uint64_t)n_blocks * a->page_tokens);
+    return plan_attention(a, false, a->n_rows, a->n_q_heads / a->n_kv_heads, (uint64_t)n_blocks * a->page_tokens, 0);
 }
 
 // The parts of AttnArgs that both operators fill alike, and the LDS.

@@ -106,6 +106,24 @@ __device__ __forceinline__ bool clear_odd(u32x4& x) {
     return odd;
 }
 
+// x of lane l joined with x of lanes l ^ 16, l ^ 32 and l ^ 48: exchanges of
+// whole rows of 16 and 32 lanes, which take no LDS round trip.
+template <class F>
+__device__ __forceinline__ float over_four(float x, F f) {
+    const uint32_t a = __float_as_uint(x);
+    const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    x = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const uint32_t b = __float_as_uint(x);
+    const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return f(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+__device__ __forceinline__ float max_over_four(float x) {
+    return over_four(x, [](float a, float b) __attribute__((always_inline)) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float sum_over_four(float x) {
+    return over_four(x, [](float a, float b) __attribute__((always_inline)) { return a + b; });
+}
+
 __device__ __forceinline__ void lds_order() { asm volatile("" ::: "memory"); }
 
 // The kernel's arguments once more.  What only rare or final steps need is
@@ -204,48 +222,45 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
             if (block >= 0 && (int64_t)block * T < len) {
                 held = (uint32_t)min(T, len - block * T);
                 const uint64_t at = ((uint64_t)seq * a.kv_heads + h) * c->table_blocks + (uint32_t)block;
-                bool missing = false;
-                auto find = [&](const int64_t* table, uint32_t n_slots, const uint32_t* bitmask, uint32_t shift)
-                                __attribute__((always_inline)) -> uint32_t {
-                    const uint32_t id = page_id(table[at], n_slots);
-                    if (id == kNoPage) {
-                        missing = true;
-                        return 0u;
-                    }
-                    comp |= page_bit(bitmask, id) << shift;
-                    return id;
-                };
-                if (S::BOTH || !only_v) id_a = find(c->k_table, c->k.n_slots, c->k.bitmask, 0);
-                if (S::BOTH) id_b = find(c->v_table, c->v.n_slots, c->v.bitmask, 1);
-                if (!S::BOTH && only_v) id_a = find(c->v_table, c->v.n_slots, c->v.bitmask, 0);
+                // both ids, then both bits, each pair in one latency
+                const bool keys = S::BOTH || !only_v, values = S::BOTH || only_v;
+                const int64_t k64 = keys ? c->k_table[at] : 0, v64 = values ? c->v_table[at] : 0;
+                const uint32_t k = page_id(k64, c->k.n_slots), v = page_id(v64, c->v.n_slots);
+                const bool missing = (keys && k == kNoPage) || (values && v == kNoPage);
+                const uint32_t k_at = !keys || k == kNoPage ? 0u : k, v_at = !values || v == kNoPage ? 0u : v;
+                const uint32_t k_word = c->k.bitmask[k_at >> 5], v_word = c->v.bitmask[v_at >> 5];
+                const uint32_t k_bit = keys && k != kNoPage ? (k_word >> (k_at & 31u)) & 1u : 0u;
+                const uint32_t v_bit = values && v != kNoPage ? (v_word >> (v_at & 31u)) & 1u : 0u;
+                id_a = S::BOTH || !only_v ? k_at : v_at;
+                id_b = v_at;
+                comp = S::BOTH ? k_bit | v_bit << 1 : k_bit | v_bit;
                 if (missing) atomicCAS(c->k.err, 0u, (uint32_t)kErrRange);
             }
         }
     };
-    // Page p of local step i -> registers: T rows of D numbers, of a slot, or
-    // of the drafted tokens' dense rows (where rows past the last token read
-    // the last one).  What they hold beyond the page's tokens is masked (keys)
-    // or cleared (values) later.
+    // The pages of local step i -> registers: T rows of D numbers each, of a
+    // slot, or of the drafted tokens' dense rows (where rows past the last
+    // token read the last one).  What they hold beyond the page's tokens is
+    // masked (keys) or cleared (values) later.
     auto load = [&](u32x4* st, uint32_t i, bool values, uint32_t ids) __attribute__((always_inline)) {
         const uint32_t s = s_first + i * kStride;
+        if (!TREE || s < ctx_steps) {
 #pragma unroll
-        for (int p = 0; p < PW; ++p) {
-            const uint32_t id = lane_value(ids, (int)((i % (64 / PW)) * PW + p));
-            const uint8_t* base = (values ? a.v.slots : a.k.slots) + (uint64_t)id * (uint64_t)(2 * D * T);
-            uint32_t row_bytes = 2 * D, last = T - 1;
-            if (TREE && s >= ctx_steps) {
-                const ArgsPtr c = args_again();
-                const uint32_t j0 = min((s - ctx_steps) * STEP + (SHARED ? page_in_step : (uint32_t)p) * T, n_new - 1);
-                base = reinterpret_cast<const uint8_t*>((values ? c->v_new : c->k_new) + (int64_t)h * c->new_head +
-                                                        (int64_t)(first_row + j0) * c->new_row);
-                row_bytes = (uint32_t)c->new_row * 2u;
-                last = min(last, n_new - 1 - j0);
-            }
+            for (int p = 0; p < PW; ++p)
+                load_page<NV>(st + p * NV, values ? a.v.slots : a.k.slots,
+                              lane_value(ids, (int)((i % (64 / PW)) * PW + p)));
+        } else {
+            const ArgsPtr c = args_again();
+            const uint16_t* base = (values ? c->v_new : c->k_new) + (int64_t)h * c->new_head;
+            const int64_t row = c->new_row;
 #pragma unroll
-            for (int r = 0; r < NV; ++r) {
-                const uint32_t w = 256u * r + 4u * lane, token = min(w / (D / 2), last), b = 4 * (w % (D / 2));
-                typedef u32x4 u32x4_any __attribute__((aligned(2)));
-                st[p * NV + r] = *reinterpret_cast<const u32x4_any*>(base + (uint64_t)token * row_bytes + b);
+            for (int p = 0; p < PW; ++p) {
+                const uint32_t j0 = (s - ctx_steps) * STEP + (SHARED ? page_in_step : (uint32_t)p) * T;
+#pragma unroll
+                for (int r = 0; r < NV; ++r) {
+                    const uint32_t w = 256u * r + 4u * lane, token = min(j0 + w / (D / 2), n_new - 1);
+                    st[p * NV + r] = load_eight(base + (int64_t)(first_row + token) * row + 2 * (w % (D / 2)));
+                }
             }
         }
     };
@@ -262,10 +277,13 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
         lds_order();
 #pragma unroll
         for (int p = 0; p < PW; ++p) {
+            const uint32_t n = values ? keep[p] : (uint32_t)T;
             if ((records >> p) & 1u) {
                 stage_page<NV>(st + p * NV, stage + p * (S::stage_bytes / 4));
+            } else if (n == (uint32_t)T) {
+#pragma unroll
+                for (int r = 0; r < NV; ++r) row_of(p, T, 256u * r + 4u * lane, st[p * NV + r]);
             } else {
-                const uint32_t n = values ? keep[p] : (uint32_t)T;
 #pragma unroll
                 for (int r = 0; r < NV; ++r) row_of(p, n, 256u * r + 4u * lane, st[p * NV + r]);
             }
@@ -314,26 +332,88 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
             for (int n = 0; n < DN; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
     }
-    if (n_steps) refill(0);
-    // tables of the record formats
-    if (4 * threadIdx.x < a.tab_words_k) reinterpret_cast<u32x4*>(smem)[threadIdx.x] = tab_k;
-    if (4 * threadIdx.x < a.tab_words_v) reinterpret_cast<u32x4*>(smem + a.tab_words_k)[threadIdx.x] = tab_v;
-    if (a.tab_words_k > 4 * kWave * kAttnWaves) stage_page_tables(a.k, smem, kWave * kAttnWaves);
-    if (a.tab_words_v > 4 * kWave * kAttnWaves) stage_page_tables(a.v, smem + a.tab_words_k, kWave * kAttnWaves);
-    if (!SHARED) __syncthreads();
+    // tables of the record formats, once the first pages are on their way
+    auto put_tables = [&]() __attribute__((always_inline)) {
+        if (4 * threadIdx.x < a.tab_words_k) reinterpret_cast<u32x4*>(smem)[threadIdx.x] = tab_k;
+        if (4 * threadIdx.x < a.tab_words_v) reinterpret_cast<u32x4*>(smem + a.tab_words_k)[threadIdx.x] = tab_v;
+        if (a.tab_words_k > 4 * kWave * kAttnWaves) stage_page_tables(a.k, smem, kWave * kAttnWaves);
+        if (a.tab_words_v > 4 * kWave * kAttnWaves) stage_page_tables(a.v, smem + a.tab_words_k, kWave * kAttnWaves);
+    };
 
-    // Iteration i works on step i - 1 and sends for step i, so that each load
-    // stands in the code once.
     u32x4 st_a[PW * NV], st_b[S::BOTH && !S::ONE ? PW * NV : 1];
     bool odd = false;
-    uint32_t n_held[PW], records = 0;  // of step i - 1: tokens of each page; which pages are records (keys, then values)
-    uint32_t ids_b = 0;                // the value pages of step i - 1 (ONE)
+    // of the step at work and of the next: tokens of each page that the wave
+    // loads, and the rows' mask words of drafted steps; which pages at work
+    // are records (keys, then values); ids of the value pages at work (ONE)
+    uint32_t n_held[PW], next_held[PW], records = 0, ids_b = 0;
+    uint32_t sees[TREE ? MR : 1][STEP / 32], next_sees[TREE ? MR : 1][STEP / 32];
+    auto facts = [&](uint32_t j) __attribute__((always_inline)) {
+        const uint32_t sn = s_first + j * kStride;
 #pragma unroll
-    for (int p = 0; p < PW; ++p) n_held[p] = 0;
-    for (uint32_t i = 0; i <= n_steps; ++i) {
-        const bool work = i > 0, more = i < n_steps;
-        const uint32_t s = s_first + (i - 1) * kStride;
-        const bool draft = TREE && work && s >= ctx_steps;
+        for (int p = 0; p < PW; ++p) {
+            next_held[p] = lane_value(held, (int)((j % (64 / PW)) * PW + p));
+            if (TREE && sn >= ctx_steps) {
+                const uint32_t j0 = (sn - ctx_steps) * STEP + (SHARED ? page_in_step : (uint32_t)p) * T;
+                next_held[p] = n_new > j0 ? min(n_new - j0, (uint32_t)T) : 0u;
+            }
+        }
+        if (TREE && sn >= ctx_steps) {
+            const ArgsPtr x = args_again();
+#pragma unroll
+            for (int t = 0; t < MR; ++t) {
+#pragma unroll
+                for (int w = 0; w < STEP / 32; ++w) {
+                    const uint32_t word = (sn - ctx_steps) * (STEP / 32) + w;
+                    next_sees[t][w] = 0;
+                    if (q_row[t] != kNoPage && word < x->mask_words2)
+                        next_sees[t][w] = x->mask[(uint64_t)q_row[t] * x->mask_words2 + word];
+                }
+            }
+        }
+    };
+    // step j becomes the one at work (after its loads have been sent: the
+    // records' bits come a latency after the ids)
+    auto advance = [&](uint32_t j) __attribute__((always_inline)) {
+        records = 0;
+        ids_b = id_b;
+#pragma unroll
+        for (int p = 0; p < PW; ++p) {
+            n_held[p] = next_held[p];
+            const uint32_t c = lane_value(comp, (int)((j % (64 / PW)) * PW + p));
+            records |= (c & 1u) << p | (c >> 1) << (PW + p);
+        }
+    };
+    auto take_sees = [&]() __attribute__((always_inline)) {
+        if constexpr (TREE) {
+#pragma unroll
+            for (int t = 0; t < MR; ++t) {
+#pragma unroll
+                for (int w = 0; w < STEP / 32; ++w) sees[t][w] = next_sees[t][w];
+            }
+        }
+    };
+#pragma unroll
+    for (int t = 0; t < (TREE ? MR : 1); ++t) {
+#pragma unroll
+        for (int w = 0; w < STEP / 32; ++w) sees[t][w] = next_sees[t][w] = 0;
+    }
+    if (n_steps) {
+        refill(0);
+        facts(0);
+        load(st_a, 0, only_v, id_a);
+        if constexpr (S::BOTH && !S::ONE) load(st_b, 0, true, id_b);
+    }
+    put_tables();
+    if (n_steps) {
+        advance(0);
+        take_sees();
+    }
+    if constexpr (!SHARED) __syncthreads();  // (the loop of SHARED begins with one)
+
+    for (uint32_t i = 0; i < n_steps; ++i) {
+        const bool more = i + 1 < n_steps;
+        const uint32_t s = s_first + i * kStride;
+        const bool draft = TREE && s >= ctx_steps;
         auto put_keys = [&]() __attribute__((always_inline)) {
             put(st_a, false, records & ((1u << PW) - 1), n_held, k_tile, S::RK);
         };
@@ -348,72 +428,35 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
             put(st, true, records >> shift, n_held, v_tile, S::RV);
         };
         if constexpr (SHARED) {
-            __syncthreads();  // the tiles are free (and the tables there)
-            if (work) {
-                if (S::BOTH) {
-                    put_keys();
-                    put_values(st_b, PW);
-                } else if (only_v) {
-                    put_values(st_a, 0);
-                } else {
-                    put_keys();
-                }
+            __syncthreads();  // the tiles are free, and the tables there
+            if (S::BOTH) {
+                put_keys();
+                put_values(st_b, PW);
+            } else if (only_v) {
+                put_values(st_a, 0);
+            } else {
+                put_keys();
             }
         } else {
-            if (work) put_keys();
+            put_keys();
         }
         const uint32_t step_held_all =
             draft ? min(n_new - (s - ctx_steps) * STEP, (uint32_t)STEP) : min((uint32_t)len - s * STEP, (uint32_t)STEP);
-        uint32_t tiles_held[!TREE && !SHARED ? PW : 1];  // tokens of the pages of step i - 1, for the masks
+        uint32_t tiles_held[!TREE && !SHARED ? PW : 1];  // tokens of the pages at work, for the masks
         if constexpr (!TREE && !SHARED) {
 #pragma unroll
             for (int p = 0; p < PW; ++p) tiles_held[p] = n_held[p];
         }
-        // step i: its pages' facts (once step i - 1's values have been put),
-        // and its loads
-        uint32_t next_held[PW], next_records = 0;
-        const uint32_t this_b = ids_b;
+        if constexpr (S::ONE) load(st_a, i, true, ids_b);
         if (more) {
-            if (i > 0 && i % (64 / PW) == 0) refill(i);
-            const uint32_t sn = s_first + i * kStride;
-#pragma unroll
-            for (int p = 0; p < PW; ++p) {
-                const int at = (int)((i % (64 / PW)) * PW + p);
-                next_held[p] = lane_value(held, at);
-                const uint32_t c = lane_value(comp, at);
-                next_records |= (c & 1u) << p | (c >> 1) << (PW + p);
-                if (TREE && sn >= ctx_steps) {
-                    const uint32_t j0 = (sn - ctx_steps) * STEP + (SHARED ? page_in_step : (uint32_t)p) * T;
-                    next_held[p] = n_new > j0 ? min(n_new - j0, (uint32_t)T) : 0u;
-                }
-            }
-            if constexpr (!S::ONE) load(st_a, i, only_v, id_a);
-            if constexpr (SHARED && S::BOTH) load(st_b, i, true, id_b);
+            if ((i + 1) % (64 / PW) == 0) refill(i + 1);
+            facts(i + 1);
+            if constexpr (!S::ONE) load(st_a, i + 1, only_v, id_a);
+            if constexpr (SHARED && S::BOTH) load(st_b, i + 1, true, id_b);
         }
-        if constexpr (S::ONE) {
-            if (work) load(st_a, i - 1, true, this_b);
-        }
-        auto advance = [&]() __attribute__((always_inline)) {
-            records = next_records;
-            ids_b = id_b;
-#pragma unroll
-            for (int p = 0; p < PW; ++p) n_held[p] = next_held[p];
-        };
         if constexpr (SHARED) {
+            if (more) advance(i + 1);
             __syncthreads();
-            if (more) advance();
-        }
-        if (!work) {
-            if constexpr (!SHARED) {
-                if (more) {
-                    if constexpr (S::ONE)
-                        load(st_a, i, false, id_a);
-                    else
-                        load(st_b, i, true, id_b);
-                    advance();
-                }
-            }
-            continue;
         }
 #pragma unroll 1
         for (uint32_t c = 0; c < (uint32_t)(STEP / S::CHUNK); ++c) {
@@ -448,7 +491,6 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
 #pragma unroll
             for (int u = 0; u < TILES; ++u) whole = whole && tile_held(u) >= 16u;
             if (!whole) {
-                const ArgsPtr x = args_again();
 #pragma unroll
                 for (int t = 0; t < MR; ++t) {
 #pragma unroll
@@ -456,10 +498,8 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
                         // bit j of `seen`: the lane's row sees token j of the tile
                         uint32_t seen = tile_held(u) >= 16u ? 0xFFFFu : (1u << tile_held(u)) - 1u;
                         if (draft) {
-                            const uint32_t word = (s - ctx_steps) * (STEP / 32) + t0 / 32 + u / 2;
-                            uint32_t bits = 0;
-                            if (q_row[t] != kNoPage && word < x->mask_words2)
-                                bits = x->mask[(uint64_t)q_row[t] * x->mask_words2 + word];
+                            uint32_t bits = sees[TREE ? t : 0][u / 2];
+                            if constexpr (STEP > S::CHUNK) bits = c ? sees[TREE ? t : 0][STEP / 64 + u / 2] : bits;
                             seen &= bits >> (16 * (u & 1));
                         }
 #pragma unroll
@@ -476,9 +516,7 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[t][u][e]);
                 }
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                top *= a.scale2;
+                top = max_over_four(top) * a.scale2;
                 // The maximum is moved only when a score passes it by more
                 // than 8 (weights then stay below 2^8 and sums far from
                 // overflow), so most steps rescale nothing.
@@ -497,8 +535,8 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
                     for (int e = 0; e < 4; ++e) {
                         const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][u][e], a.scale2, base));
                         sc[t][u][e] = p;
-                        l[t] += p;
                     }
+                    l[t] += (sc[t][u][0] + sc[t][u][1]) + (sc[t][u][2] + sc[t][u][3]);
                 }
             }
 
@@ -506,10 +544,10 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
             if constexpr (!SHARED) {
                 if (more) {
                     if constexpr (S::ONE)
-                        load(st_a, i, false, id_a);
+                        load(st_a, i + 1, false, id_a);
                     else
-                        load(st_b, i, true, id_b);
-                    advance();
+                        load(st_b, i + 1, true, id_b);
+                    advance(i + 1);
                 }
             }
             // O^T += V^T P^T
@@ -534,6 +572,7 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
             }
             lds_order();
         }
+        if (more) take_sees();
     }
 
     // --- the sums over the four lanes of a row, then the result or this split's part
@@ -558,8 +597,7 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
     };
 #pragma unroll
     for (int t = 0; t < MR; ++t) {
-        l[t] += __shfl_xor(l[t], 16);
-        l[t] += __shfl_xor(l[t], 32);
+        l[t] = sum_over_four(l[t]);
         if constexpr (SHARED) {
             uint32_t j;
             const uint32_t row = row_head(row0 + 16 * t + col, &j);

@@ -425,6 +425,21 @@ def ibp_gather_decompress_split(meta: Meta, slots: torch.Tensor, n_slots: int, h
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
+def _addr(t: torch.Tensor | None):
+    """Address of a tensor whose layout the call describes; an int, which
+    ctypes takes for a pointer without an object of its own."""
+    return None if t is None else t.data_ptr()
+
+
+def _flat(t: torch.Tensor | None):
+    """Address of a contiguous tensor."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libibp must be contiguous")
+    return t.data_ptr()
+
+
 class Pages:
     """A pool of pages: the slots and bitmask that ibp_compress writes, and
     the handle of their format.  Keeps the tensors alive; `slots` may be any
@@ -435,7 +450,7 @@ class Pages:
         _need(bitmask, _bitmask_bytes(n_slots), "bitmask")
         self.meta, self.slots, self.n_slots, self.bitmask = meta, slots, int(n_slots), bitmask
         self.tensor_bytes = meta.tensor_bytes
-        self._struct = ibp_pages(meta.handle, _ptr(slots), self.n_slots, _ptr(bitmask))
+        self._struct = ibp_pages(meta.handle, _flat(slots), self.n_slots, _flat(bitmask))
 
     @property
     def _as_parameter_(self):
@@ -451,11 +466,11 @@ def _typed(t: torch.Tensor, dtype: torch.dtype, what: str, numel: int | None = N
         raise ValueError(f"{what} holds {t.numel()} entries, the call needs {numel}")
 
 
-def _stream_of(stream, t: torch.Tensor) -> ctypes.c_void_p:
+def _stream_of(stream, t: torch.Tensor):
     if stream is not None:
-        return ctypes.c_void_p(stream.cuda_stream)
+        return stream.cuda_stream
     if _raw_stream is not None and t.is_cuda:
-        return ctypes.c_void_p(_raw_stream(t.device.index))
+        return _raw_stream(t.get_device())
     return _stream(None)
 
 
@@ -487,8 +502,8 @@ def ibp_pages_copy(meta: Meta, src_slots: torch.Tensor, n_src: int, src_bitmask:
     L = meta.tensor_bytes
     _need_all((src_slots, int(n_src) * L, "src_slots"), (dst_slots, int(n_dst) * L, "dst_slots"),
               (src_bitmask, _bitmask_bytes(n_src), "src_bitmask"), (dst_bitmask, _bitmask_bytes(n_dst), "dst_bitmask"))
-    _check(lib().ibp_pages_copy(meta, _ptr(src_slots), int(n_src), _ptr(src_bitmask), _ptr(src_ids), _ptr(dst_slots),
-                                int(n_dst), _ptr(dst_bitmask), _ptr(dst_ids), src_ids.numel(),
+    _check(lib().ibp_pages_copy(meta, _flat(src_slots), int(n_src), _flat(src_bitmask), _flat(src_ids), _flat(dst_slots),
+                                int(n_dst), _flat(dst_bitmask), _flat(dst_ids), src_ids.numel(),
                                 _stream_of(stream, src_ids)), "ibp_pages_copy")
 
 
@@ -501,7 +516,7 @@ def ibp_pages_alloc(meta: Meta, refs: torch.Tensor, n_slots: int, ids: torch.Ten
     _typed(refs, torch.int32, "refs", int(n_slots))
     _typed(ids, torch.int64, "ids")
     ws = _workspace(workspace, ibp_pages_workspace(n_slots), refs, stream)
-    _check(lib().ibp_pages_alloc(meta, _ptr(refs), int(n_slots), _ptr(ids), ids.numel(), _ptr(ws), _bytes_of(ws),
+    _check(lib().ibp_pages_alloc(meta, _flat(refs), int(n_slots), _flat(ids), ids.numel(), _flat(ws), _bytes_of(ws),
                                  _stream_of(stream, refs)), "ibp_pages_alloc")
 
 
@@ -525,8 +540,8 @@ def ibp_pages_fork(meta: Meta, slots: torch.Tensor, n_slots: int, bitmask: torch
     _typed(children, torch.int64, "children", n)
     _need_all((slots, int(n_slots) * meta.tensor_bytes, "slots"), (bitmask, _bitmask_bytes(n_slots), "bitmask"))
     ws = _workspace(workspace, ibp_pages_workspace(n_slots, n * heads), refs, stream)
-    _check(lib().ibp_pages_fork(meta, _ptr(slots), int(n_slots), _ptr(bitmask), _ptr(refs), _ptr(table), n_seqs, heads,
-                                blocks, _ptr(lens), int(page_tokens), _ptr(parents), _ptr(children), n, _ptr(ws),
+    _check(lib().ibp_pages_fork(meta, _flat(slots), int(n_slots), _flat(bitmask), _flat(refs), _flat(table), n_seqs, heads,
+                                blocks, _flat(lens), int(page_tokens), _flat(parents), _flat(children), n, _flat(ws),
                                 _bytes_of(ws), _stream_of(stream, refs)), "ibp_pages_fork")
 
 
@@ -535,7 +550,7 @@ def ibp_pages_free(meta: Meta, refs: torch.Tensor, n_slots: int, table: torch.Te
     n_seqs, heads, blocks = _table_shape(table)
     _typed(refs, torch.int32, "refs", int(n_slots))
     _typed(seqs, torch.int64, "seqs")
-    _check(lib().ibp_pages_free(meta, _ptr(refs), int(n_slots), _ptr(table), n_seqs, heads, blocks, _ptr(seqs),
+    _check(lib().ibp_pages_free(meta, _flat(refs), int(n_slots), _flat(table), n_seqs, heads, blocks, _flat(seqs),
                                 seqs.numel(), _stream_of(stream, refs)), "ibp_pages_free")
 
 
@@ -551,8 +566,8 @@ def ibp_pages_compact(meta: Meta, slots: torch.Tensor, n_slots: int, bitmask: to
         _typed(table, torch.int64, "table")
     _need_all((slots, int(n_slots) * meta.tensor_bytes, "slots"), (bitmask, _bitmask_bytes(n_slots), "bitmask"))
     ws = _workspace(workspace, ibp_pages_workspace(n_slots), refs, stream)
-    _check(lib().ibp_pages_compact(meta, _ptr(slots), int(n_slots), _ptr(bitmask), _ptr(refs), _ptr(map), _ptr(n_live),
-                                   _ptr(table), 0 if table is None else table.numel(), _ptr(ws), _bytes_of(ws),
+    _check(lib().ibp_pages_compact(meta, _flat(slots), int(n_slots), _flat(bitmask), _flat(refs), _flat(map), _flat(n_live),
+                                   _flat(table), 0 if table is None else table.numel(), _flat(ws), _bytes_of(ws),
                                    _stream_of(stream, refs)), "ibp_pages_compact")
 
 
@@ -562,11 +577,14 @@ def _queries(q: torch.Tensor, table: torch.Tensor, page_tokens: int, scale: floa
     if q.dtype not in _DTYPES:
         raise ValueError(f"q must be bfloat16 or float16, not {q.dtype}")
     n_seqs, kv_heads, blocks = _table_shape(table)
-    if q.dim() != 3 or (q.shape[2] > 1 and q.stride(2) != 1):
-        raise ValueError("q has the shape (rows, heads, dims) with contiguous dims")
-    return ibp_attention(dtype=_DTYPES[q.dtype], head_dim=q.shape[2], page_tokens=int(page_tokens),
-                         n_q_heads=q.shape[1], n_kv_heads=kv_heads, scale=float(scale), n_rows=q.shape[0],
-                         n_seqs=n_seqs, table_blocks=blocks, q_row_stride=q.stride(0), q_head_stride=q.stride(1))
+    if q.dim() != 3:
+        raise ValueError("q has the shape (rows, heads, dims)")
+    rows, heads, dim = q.shape
+    row_stride, head_stride, dim_stride = q.stride()
+    if dim > 1 and dim_stride != 1:
+        raise ValueError("q's dims must be contiguous")
+    return ibp_attention(_DTYPES[q.dtype], dim, int(page_tokens), heads, kv_heads, scale, rows, n_seqs, blocks, 0, 0,
+                         row_stride, head_stride, 0, 0)
 
 
 def _outputs(q, out, lse, k: Pages, v: Pages):
@@ -583,8 +601,6 @@ def _outputs(q, out, lse, k: Pages, v: Pages):
     return k.tensor_bytes // row
 
 
-def _dense_ptr(t: torch.Tensor):
-    return ctypes.c_void_p(t.data_ptr())
 
 
 def ibp_tree_attention(k: Pages, v: Pages, q: torch.Tensor, k_table: torch.Tensor, v_table: torch.Tensor,
@@ -613,9 +629,9 @@ def ibp_tree_attention(k: Pages, v: Pages, q: torch.Tensor, k_table: torch.Tenso
     a.max_len, a.max_new = int(max_len), int(max_new)
     ref = ctypes.byref(a)
     ws = _workspace(workspace, int(lib().ibp_tree_attention_workspace(ref)), q, stream)
-    _check(lib().ibp_tree_attention(k, v, ref, _dense_ptr(q), _ptr(k_table), _ptr(v_table), _ptr(lens), _ptr(new_rows),
-                                    _dense_ptr(k_new), _dense_ptr(v_new), _ptr(mask), mask.shape[1], _ptr(out),
-                                    _ptr(lse), _ptr(ws), _bytes_of(ws), _stream_of(stream, q)), "ibp_tree_attention")
+    _check(lib().ibp_tree_attention(k, v, ref, _addr(q), _flat(k_table), _flat(v_table), _flat(lens), _flat(new_rows),
+                                    _addr(k_new), _addr(v_new), _flat(mask), mask.shape[1], _flat(out),
+                                    _flat(lse), _flat(ws), _bytes_of(ws), _stream_of(stream, q)), "ibp_tree_attention")
 
 
 def ibp_page_bounds(k: Pages, ids: torch.Tensor, tokens: torch.Tensor | None, bounds: torch.Tensor, stream=None):
@@ -626,8 +642,8 @@ def ibp_page_bounds(k: Pages, ids: torch.Tensor, tokens: torch.Tensor | None, bo
         raise ValueError("bounds must be bfloat16 or float16 of shape (slots, 2, dims)")
     if tokens is not None:
         _typed(tokens, torch.int32, "tokens", ids.numel())
-    _check(lib().ibp_page_bounds(k, _DTYPES[bounds.dtype], bounds.shape[2], _ptr(ids), _ptr(tokens), ids.numel(),
-                                 _ptr(bounds), _stream_of(stream, ids)), "ibp_page_bounds")
+    _check(lib().ibp_page_bounds(k, _DTYPES[bounds.dtype], bounds.shape[2], _flat(ids), _flat(tokens), ids.numel(),
+                                 _flat(bounds), _stream_of(stream, ids)), "ibp_page_bounds")
 
 
 def _rows_of(a: ibp_attention, lens, row_seq):
@@ -658,8 +674,8 @@ def ibp_select_pages(q: torch.Tensor, bounds: torch.Tensor, k_table: torch.Tenso
     n = _block_lists(a, blocks)
     ref = ctypes.byref(a)
     ws = _workspace(workspace, int(lib().ibp_select_pages_workspace(ref)), q, stream)
-    _check(lib().ibp_select_pages(meta, ref, _dense_ptr(q), _ptr(bounds), bounds.shape[0], _ptr(k_table), _ptr(lens),
-                                  _ptr(row_seq), int(keep_first), int(keep_last), _ptr(blocks), n, _ptr(ws),
+    _check(lib().ibp_select_pages(meta, ref, _addr(q), _flat(bounds), bounds.shape[0], _flat(k_table), _flat(lens),
+                                  _flat(row_seq), int(keep_first), int(keep_last), _flat(blocks), n, _flat(ws),
                                   _bytes_of(ws), _stream_of(stream, q)), "ibp_select_pages")
 
 
@@ -675,6 +691,6 @@ def ibp_sparse_attention(k: Pages, v: Pages, q: torch.Tensor, k_table: torch.Ten
     n = _block_lists(a, blocks)
     ref = ctypes.byref(a)
     ws = _workspace(workspace, int(lib().ibp_sparse_attention_workspace(ref, n)), q, stream)
-    _check(lib().ibp_sparse_attention(k, v, ref, _dense_ptr(q), _ptr(k_table), _ptr(v_table), _ptr(lens),
-                                      _ptr(row_seq), _ptr(blocks), n, _ptr(out), _ptr(lse), _ptr(ws), _bytes_of(ws),
+    _check(lib().ibp_sparse_attention(k, v, ref, _addr(q), _flat(k_table), _flat(v_table), _flat(lens),
+                                      _flat(row_seq), _flat(blocks), n, _flat(out), _flat(lse), _flat(ws), _bytes_of(ws),
                                       _stream_of(stream, q)), "ibp_sparse_attention")
