@@ -13,16 +13,10 @@ using namespace ibp;
 
 namespace {
 
-// Workgroups that a launch should have: two per compute unit of an MI355X.
-constexpr uint64_t kTargetGroups = 512;
+// Waves that a launch should have: eight per compute unit of an MI355X.
+constexpr uint64_t kTargetWaves = 2048;
 constexpr uint64_t kMaxSplits = 256;
 constexpr uint64_t kLdsLimit = 160 * 1024 - 2048;  // the kernels' static arrays aside
-
-template <int D, int T, bool SHARED>
-void shape_of(AttnPlan* p) {
-    p->step = AttnShape<D, T, SHARED>::STEP;
-    p->area_bytes = AttnShape<D, T, SHARED>::area_bytes;
-}
 
 // Rows per workgroup, split of the context, LDS.  `rows`: most rows of one
 // (sequence or row, key/value head).
@@ -31,16 +25,15 @@ AttnPlan plan_attention(const ibp_attention* a, bool tree, uint64_t items, uint6
     AttnPlan p;
     const uint32_t D = a->head_dim, T = a->page_tokens;
     const uint32_t m2 = D <= 128 ? 2 : 1;
-    p.shared = tree && rows > 16 * m2;
-    p.mr = rows <= (p.shared ? 64u : 16u) ? 1 : 2;
-    const uint64_t per_wg = 16ull * (p.mr == 1 ? 1 : m2) * (p.shared ? kAttnWaves : 1);
+    p.many = tree && rows > 16 * m2;
+    const uint32_t waves = p.many ? kManyWaves : kFewWaves;
+    p.mr = rows <= (p.many ? 16u * kManyWaves : 16u) ? 1 : 2;
+    const uint64_t per_wg = 16ull * (p.mr == 1 ? 1 : m2) * (p.many ? kManyWaves : 1);
     p.row_tiles = (uint32_t)((rows + per_wg - 1) / per_wg);
-#define IBP_SHAPE(DD, TT)                         \
-    if (D == DD && T == TT) {                     \
-        if (p.shared)                             \
-            shape_of<DD, TT, true>(&p);           \
-        else                                      \
-            shape_of<DD, TT, false>(&p);          \
+#define IBP_SHAPE(DD, TT)                                                                      \
+    if (D == DD && T == TT) {                                                                  \
+        p.step = p.many ? ManyShape<DD, TT>::STEP : FewShape<DD, TT>::STEP;                    \
+        p.area_bytes = p.many ? ManyShape<DD, TT>::area_bytes : FewShape<DD, TT>::area_bytes;  \
     }
     IBP_SHAPE(64, 16)
     IBP_SHAPE(64, 32)
@@ -51,9 +44,10 @@ AttnPlan plan_attention(const ibp_attention* a, bool tree, uint64_t items, uint6
 #undef IBP_SHAPE
     const uint64_t steps = (tokens + p.step - 1) / p.step + (new_tokens + p.step - 1) / p.step;
     const uint64_t groups = items * a->n_kv_heads * p.row_tiles;
-    const uint64_t least = p.shared ? 2 : kAttnWaves;  // steps that make a split worth joining
+    const uint64_t target = kTargetWaves / waves;
+    const uint64_t least = p.many ? 2 : kFewWaves;  // steps that make a split worth joining
     const uint64_t most = std::max<uint64_t>(1, (steps + least - 1) / least);
-    p.splits = (uint32_t)std::min({most, (kTargetGroups + groups - 1) / groups, kMaxSplits});
+    p.splits = (uint32_t)std::min({most, (target + groups - 1) / groups, kMaxSplits});
     return p;
 }
 

@@ -16,13 +16,17 @@
 // of tokens, padded so that the operand reads spread over the banks.  The next
 // page's loads are in flight meanwhile.
 //
-// Two shapes of work:
-//   SHARED = false: few rows (16 MR).  Every wave walks pages of its own for
-//     all rows, without a barrier, and the waves' results are joined at the
-//     end.  Bound by the pages' bytes (or their rebuild).
-//   SHARED = true: many rows.  The workgroup's waves load a step's pages
-//     together, each rebuilding its share, and each multiplies all of them
-//     with 16 MR rows of its own.
+// Two kernels:
+//   k_attend_few, up to 16 MR rows.  Every wave walks pages of its own for all
+//     rows, without a barrier, and the waves' results are joined at the end.
+//     Bound by the pages' bytes, or by latency when there are few of them.
+//   k_attend_many.  Four waves with 16 MR rows each share a step's pages,
+//     which they load and rebuild between them; two such workgroups on a
+//     compute unit overlap one's rebuilding with the other's products.  (Eight
+//     waves with two buffers and one barrier per step, measured: the waves
+//     that rebuild hold up all others; eight streams of 24 drafted tokens over
+//     8 K 140 us instead of 86, two 64 K contexts with 64 drafted tokens,
+//     nothing to rebuild, 470 us instead of 420.)
 // A long context is split over workgroups; k_join adds the parts.
 #pragma once
 
@@ -35,7 +39,8 @@ namespace ibp {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr uint32_t kAttnWaves = 4;
+constexpr uint32_t kFewWaves = 4;
+constexpr uint32_t kManyWaves = 4;
 
 struct AttnArgs {
     Pool k, v;
@@ -73,23 +78,39 @@ __device__ __forceinline__ u32x2 read_transposed(const char* lds) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)lds));
 }
 
-template <int D, int T, bool SHARED>
-struct AttnShape {
-    static constexpr int NV = D * T / 512;                 // vectors per lane of a page
-    static constexpr int STEP = SHARED ? (T == 64 ? 128 : 64) : (T < 32 ? 32 : T);
-    static constexpr int PP = STEP / T;                    // pages per step
-    static constexpr bool BOTH = !SHARED || T == 16;       // a wave loads keys and values
-    static constexpr int PW = SHARED ? 1 : PP;             // pages per step, wave and kind
-    static constexpr int RK = 2 * D + 16, RV = 2 * D + 32; // bytes per token row in LDS
+// Sizes of the two kernels.  A token's row in LDS is padded so that the reads
+// of 16 tokens (keys) and of four tokens at a time (values) spread over all
+// banks.
+template <int D, int T>
+struct PageShape {
+    static constexpr int NV = D * T / 512;                  // vectors per lane of a page
+    static constexpr int U = 2;                             // steps of a rebuild taken together
+    static constexpr int RK = 2 * D + 16, RV = 2 * D + 32;  // bytes per token row in LDS
     static constexpr uint32_t stage_bytes = 4 * page_stage_words<NV>();
-    static constexpr int CHUNK = SHARED ? 64 : STEP;       // tokens per pass of the softmax
-    static constexpr bool ONE = !SHARED && PW * NV > 8;    // one register buffer for keys and values in turn
-    static constexpr uint32_t wave_bytes = PW * stage_bytes + (SHARED ? 0 : STEP * RV);
     static_assert(stage_bytes % 16 == 0, "areas are vectors");
-    static constexpr uint32_t shared_bytes = SHARED ? STEP * (RK + RV) : 0;
-    static constexpr uint32_t join_bytes = SHARED ? 0 : kAttnWaves * (16 * (D + 4) * 4);
-    static constexpr uint32_t area_bytes =
-        kAttnWaves * wave_bytes + shared_bytes > join_bytes ? kAttnWaves * wave_bytes + shared_bytes : join_bytes;
+};
+
+template <int D, int T>
+struct FewShape : PageShape<D, T> {
+    using P = PageShape<D, T>;
+    static constexpr int STEP = T < 32 ? 32 : T;            // tokens per step of a wave
+    static constexpr int PW = STEP / T;                     // pages of each kind
+    static constexpr bool ONE = PW * P::NV > 8;             // one register buffer for keys and values in turn
+    static constexpr uint32_t wave_bytes = PW * P::stage_bytes + STEP * P::RV;
+    static constexpr uint32_t join_bytes = kFewWaves * 16 * (D + 4) * 4;
+    static constexpr uint32_t area_bytes = kFewWaves * wave_bytes > join_bytes ? kFewWaves * wave_bytes : join_bytes;
+};
+
+template <int D, int T>
+struct ManyShape : PageShape<D, T> {
+    using P = PageShape<D, T>;
+    static constexpr int STEP = 64;                         // tokens per step of the workgroup
+    static constexpr int KP = STEP / T;                     // pages of each kind
+    static constexpr bool BOTH = KP == kManyWaves;          // every wave has a page of each kind
+    static constexpr int JOBS = BOTH ? KP : 2 * KP;         // waves that a step's pages take
+    static constexpr int ROUNDS = kManyWaves / JOBS;        // a wave loads for every ROUNDS-th step
+    static constexpr uint32_t tile_bytes = STEP * (P::RK + P::RV);
+    static constexpr uint32_t area_bytes = tile_bytes + JOBS * P::stage_bytes;
 };
 
 // Infinities and NaNs of eight numbers become zero; whether there was one.
@@ -137,194 +158,140 @@ __device__ __forceinline__ ArgsPtr args_again() {
     return p;
 }
 
-template <class E, int D, int T, int MR, bool SHARED, bool TREE>
-__global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
-    using S = AttnShape<D, T, SHARED>;
-    using V8 = typename E::V8;
-    constexpr int NV = S::NV, STEP = S::STEP, PP = S::PP, PW = S::PW, TILES = S::CHUNK / 16;
-    constexpr int DK = D / 32, DN = D / 16;
-    constexpr uint32_t kRowsWg = 16u * MR * (SHARED ? kAttnWaves : 1u);
-    constexpr uint32_t kStride = SHARED ? 1u : kAttnWaves;  // steps between a wave's steps
-    extern __shared__ __align__(16) uint32_t smem[];
-    __shared__ float join_m[kAttnWaves][16], join_l[kAttnWaves][16];
-    __shared__ uint32_t odd_values;  // an infinity or NaN among the drafted values
-    const uint32_t lane = lane_id(), wib = uniform(threadIdx.x / kWave);
-    const uint32_t col = lane & 15u, g = lane >> 4;
+// What a workgroup works on.
+struct Work {
+    uint32_t split, h, item, rt;           // split, key/value head, sequence (tree) or row, row tile
+    uint32_t seq, first_row, n_new, rows;  // rows: query heads of the group times drafted tokens (or one)
+    int32_t len;
+};
 
-    // the first vector per thread of each pool's tables is on its way while
-    // the wave finds its pages
-    u32x4 tab_k = {0u, 0u, 0u, 0u}, tab_v = {0u, 0u, 0u, 0u};
-    if (4 * threadIdx.x < a.tab_words_k) tab_k = page_table_vector(a.k, threadIdx.x);
-    if (4 * threadIdx.x < a.tab_words_v) tab_v = page_table_vector(a.v, threadIdx.x);
-    if (TREE && threadIdx.x == 0) odd_values = 0;
-
-    // which part of the work: split, (sequence or row, head), row tile
-    const uint32_t split = blockIdx.x % a.splits;
-    const uint32_t wg = (blockIdx.x / a.splits) % a.work, rt = blockIdx.x / a.splits / a.work;
-    const uint32_t h = wg % a.kv_heads;
-    const uint32_t item = wg / a.kv_heads;  // sequence (tree) or row
-    uint32_t seq = item, first_row = TREE ? 0u : item, n_new = TREE ? 0u : 1u;
-    int32_t len = a.lens[item];
-    bool bad = len < 0 || (uint64_t)len > a.table_blocks * T;
+// False when there is nothing to do; what is not valid latches kErrRange.
+template <int T, bool TREE>
+__device__ __forceinline__ bool find_work(const AttnArgs& a, uint32_t rows_per_wg, Work& w) {
+    w.split = blockIdx.x % a.splits;
+    const uint32_t wg = (blockIdx.x / a.splits) % a.work;
+    w.rt = blockIdx.x / a.splits / a.work;
+    w.h = wg % a.kv_heads;
+    w.item = wg / a.kv_heads;
+    w.seq = w.item;
+    w.first_row = TREE ? 0u : w.item;
+    w.n_new = TREE ? 0u : 1u;
+    w.len = a.lens[w.item];
+    bool bad = w.len < 0 || (uint64_t)w.len > a.table_blocks * T;
     if (TREE) {
-        const int32_t r0 = a.new_rows[item], r1 = a.new_rows[item + 1];
+        const int32_t r0 = a.new_rows[w.item], r1 = a.new_rows[w.item + 1];
         const uint32_t n = (uint32_t)(r1 - r0);
         if (r0 < 0 || r1 < r0 || (uint64_t)r1 > a.n_rows || n > a.max_new || n > 32u * a.mask_words2) {
             bad = true;
         } else {
-            first_row = (uint32_t)r0;
-            n_new = n;
+            w.first_row = (uint32_t)r0;
+            w.n_new = n;
         }
     } else if (a.row_seq) {
-        const int32_t s = a.row_seq[item];
+        const int32_t s = a.row_seq[w.item];
         bad = bad || s < 0 || (uint64_t)s >= a.n_seqs;
-        seq = (uint32_t)s;
+        w.seq = (uint32_t)s;
     }
     if (bad) {
         latch_error(a.k.err, kErrRange);
-        if (TREE) return;
-        seq = 0;
-        len = 0;
+        if (TREE) return false;
+        w.seq = 0;
+        w.len = 0;
     }
-    const uint32_t rows = n_new * a.group;
-    if (rt * kRowsWg >= rows) return;
-    const uint32_t row0 = rt * kRowsWg + (SHARED ? wib * 16u * MR : 0u);
+    w.rows = w.n_new * a.group;
+    return w.rt * rows_per_wg < w.rows;
+}
 
-    // steps of this split: the context's, then the drafted tokens'
-    const uint32_t ctx_pages = TREE ? ((uint32_t)len + T - 1) / T : (len > 0 ? a.n_list : 0u);
-    const uint32_t ctx_steps = (ctx_pages + PP - 1) / PP;
-    const uint32_t all_steps = ctx_steps + (TREE ? (n_new + STEP - 1) / STEP : 0u);
-    const uint32_t per = (all_steps + a.splits - 1) / a.splits;
-    const uint32_t s_lo = min(split * per, all_steps), s_hi = min(s_lo + per, all_steps);
-    const uint32_t s_first = s_lo + (SHARED ? 0u : wib);
-    const uint32_t n_steps = s_first < s_hi ? (s_hi - s_first + kStride - 1) / kStride : 0u;
+// The drafted token and query head of row rho of the group.
+__device__ __forceinline__ uint32_t row_of_group(const AttnArgs& a, const Work& w, uint32_t rho, uint32_t* head) {
+    const uint32_t i = rho / a.group;
+    *head = w.h * a.group + (rho - i * a.group);
+    return w.first_row + i;
+}
 
-    char* const area = reinterpret_cast<char*>(smem + a.tab_words_k + a.tab_words_v);
-    uint32_t* const stage = reinterpret_cast<uint32_t*>(area + wib * S::wave_bytes);
-    char* const k_tile =
-        SHARED ? area + kAttnWaves * S::wave_bytes : reinterpret_cast<char*>(stage) + PW * S::stage_bytes;
-    char* const v_tile = SHARED ? k_tile + STEP * S::RK : k_tile;
+// First vector per thread of each pool's tables, on its way while a wave
+// finds its pages; and the tables' place in LDS.
+struct EarlyTables {
+    u32x4 k, v;
+    __device__ __forceinline__ void load(const AttnArgs& a) {
+        k = v = u32x4{0u, 0u, 0u, 0u};
+        if (4 * threadIdx.x < a.tab_words_k) k = page_table_vector(a.k, threadIdx.x);
+        if (4 * threadIdx.x < a.tab_words_v) v = page_table_vector(a.v, threadIdx.x);
+    }
+    __device__ __forceinline__ void put(const AttnArgs& a, uint32_t* smem) const {
+        if (4 * threadIdx.x < a.tab_words_k) reinterpret_cast<u32x4*>(smem)[threadIdx.x] = k;
+        if (4 * threadIdx.x < a.tab_words_v) reinterpret_cast<u32x4*>(smem + a.tab_words_k)[threadIdx.x] = v;
+        if (a.tab_words_k > 4 * blockDim.x) stage_page_tables(a.k, smem, blockDim.x);
+        if (a.tab_words_v > 4 * blockDim.x) stage_page_tables(a.v, smem + a.tab_words_k, blockDim.x);
+    }
+};
 
-    // a wave of SHARED pages of 32 or 64 tokens loads keys or values only
-    const bool only_v = !S::BOTH && (wib & 1u);
-    const uint32_t page_in_step = SHARED ? (T == 16 ? wib : wib >> 1) : 0u;
+__device__ __forceinline__ PageTab kind_tab(const AttnArgs& a, const uint32_t* smem, bool values) {
+    return page_tab(values ? a.v : a.k, smem + (values && !a.same_tab ? a.tab_words_k : 0u),
+                    values ? a.tab_lds_v : a.tab_lds_k);
+}
 
-    // --- the wave's next pages: lane l has page l % PW of its step base + l / PW
-    uint32_t id_a = 0, id_b = 0, held = 0, comp = 0;
-    auto refill = [&](uint32_t base) __attribute__((always_inline)) {
-        const ArgsPtr c = args_again();
-        const uint32_t s = s_first + (base + lane / PW) * kStride;
-        id_a = id_b = held = comp = 0;
-        if (s < s_hi && s < ctx_steps) {
-            const uint32_t n = s * PP + (SHARED ? page_in_step : lane % PW);
-            int32_t block = n < ctx_pages ? (int32_t)n : -1;
-            if (!TREE && n < ctx_pages) block = c->blocks[((uint64_t)item * a.kv_heads + h) * c->n_list + n];
-            if (block >= 0 && (int64_t)block * T < len) {
-                held = (uint32_t)min(T, len - block * T);
-                const uint64_t at = ((uint64_t)seq * a.kv_heads + h) * c->table_blocks + (uint32_t)block;
-                // both ids, then both bits, each pair in one latency
-                const bool keys = S::BOTH || !only_v, values = S::BOTH || only_v;
-                const int64_t k64 = keys ? c->k_table[at] : 0, v64 = values ? c->v_table[at] : 0;
-                const uint32_t k = page_id(k64, c->k.n_slots), v = page_id(v64, c->v.n_slots);
-                const bool missing = (keys && k == kNoPage) || (values && v == kNoPage);
-                const uint32_t k_at = !keys || k == kNoPage ? 0u : k, v_at = !values || v == kNoPage ? 0u : v;
-                const uint32_t k_word = c->k.bitmask[k_at >> 5], v_word = c->v.bitmask[v_at >> 5];
-                const uint32_t k_bit = keys && k != kNoPage ? (k_word >> (k_at & 31u)) & 1u : 0u;
-                const uint32_t v_bit = values && v != kNoPage ? (v_word >> (v_at & 31u)) & 1u : 0u;
-                id_a = S::BOTH || !only_v ? k_at : v_at;
-                id_b = v_at;
-                comp = S::BOTH ? k_bit | v_bit << 1 : k_bit | v_bit;
-                if (missing) atomicCAS(c->k.err, 0u, (uint32_t)kErrRange);
-            }
-        }
-    };
-    // The pages of local step i -> registers: T rows of D numbers each, of a
-    // slot, or of the drafted tokens' dense rows (where rows past the last
-    // token read the last one).  What they hold beyond the page's tokens is
-    // masked (keys) or cleared (values) later.
-    auto load = [&](u32x4* st, uint32_t i, bool values, uint32_t ids) __attribute__((always_inline)) {
-        const uint32_t s = s_first + i * kStride;
-        if (!TREE || s < ctx_steps) {
+// One wave: T rows from token j0 of the drafted tokens' keys or values, as
+// load_page lays out a page; rows past the last token read the last one.
+template <int D, int NV>
+__device__ __forceinline__ void load_drafted(u32x4* st, const Work& w, bool values, uint32_t j0) {
+    const ArgsPtr c = args_again();
+    const uint16_t* base = (values ? c->v_new : c->k_new) + (int64_t)w.h * c->new_head;
+    const int64_t row = c->new_row;
 #pragma unroll
-            for (int p = 0; p < PW; ++p)
-                load_page<NV>(st + p * NV, values ? a.v.slots : a.k.slots,
-                              lane_value(ids, (int)((i % (64 / PW)) * PW + p)));
-        } else {
-            const ArgsPtr c = args_again();
-            const uint16_t* base = (values ? c->v_new : c->k_new) + (int64_t)h * c->new_head;
-            const int64_t row = c->new_row;
-#pragma unroll
-            for (int p = 0; p < PW; ++p) {
-                const uint32_t j0 = (s - ctx_steps) * STEP + (SHARED ? page_in_step : (uint32_t)p) * T;
-#pragma unroll
-                for (int r = 0; r < NV; ++r) {
-                    const uint32_t w = 256u * r + 4u * lane, token = min(j0 + w / (D / 2), n_new - 1);
-                    st[p * NV + r] = load_eight(base + (int64_t)(first_row + token) * row + 2 * (w % (D / 2)));
-                }
-            }
-        }
-    };
-    // The wave's pages as rows of tokens in LDS.  A record goes through the
-    // stage; values behind a page's last token become zero.  Lane-wise words
-    // of a page: four at w, of token w / (D / 2).
-    auto put = [&](const u32x4* st, bool values, uint32_t records, const uint32_t* keep, char* tile, int stride)
-                   __attribute__((always_inline)) {
-        auto row_of = [&](uint32_t p, uint32_t n, uint32_t w, u32x4 x) __attribute__((always_inline)) {
-            const uint32_t token = w / (D / 2), b = 4 * (w % (D / 2));
-            if (token >= n) x = u32x4{0u, 0u, 0u, 0u};
-            *reinterpret_cast<u32x4*>(tile + ((SHARED ? page_in_step : p) * T + token) * stride + b) = x;
-        };
-        lds_order();
-#pragma unroll
-        for (int p = 0; p < PW; ++p) {
-            const uint32_t n = values ? keep[p] : (uint32_t)T;
-            if ((records >> p) & 1u) {
-                stage_page<NV>(st + p * NV, stage + p * (S::stage_bytes / 4));
-            } else if (n == (uint32_t)T) {
-#pragma unroll
-                for (int r = 0; r < NV; ++r) row_of(p, T, 256u * r + 4u * lane, st[p * NV + r]);
-            } else {
-#pragma unroll
-                for (int r = 0; r < NV; ++r) row_of(p, n, 256u * r + 4u * lane, st[p * NV + r]);
-            }
-        }
-        const Pool& pool = values ? a.v : a.k;
-        const PageTab tab = page_tab(pool, smem + (values && !a.same_tab ? a.tab_words_k : 0u),
-                                     values ? a.tab_lds_v : a.tab_lds_k);
-        for (; records; records &= records - 1) {
-            const uint32_t p = PW == 1 ? 0u : (uint32_t)__builtin_ctz(records);
-            const uint32_t n = !values ? (uint32_t)T : PW == 1 || p == 0 ? keep[0] : keep[PW - 1];
-            if (!rebuild_page<NV>(pool, tab, stage + p * (S::stage_bytes / 4),
-                                  [&](uint32_t w, u32x4 x) __attribute__((always_inline)) { row_of(p, n, w, x); }))
-                latch_error(args_again()->k.err, kErrCorrupt);
-        }
-        lds_order();
-    };
+    for (int r = 0; r < NV; ++r) {
+        const uint32_t x = 256u * r + 4u * lane_id(), token = min(j0 + x / (D / 2), w.n_new - 1);
+        st[r] = load_eight(base + (int64_t)(w.first_row + token) * row + 2 * (x % (D / 2)));
+    }
+}
 
-    // --- the rows' queries (B operand) and running state
-    V8 qf[MR][DK];
+// Words x of a page (four from word at) to its rows of tokens in LDS; tokens
+// from n on become zero.
+template <int D>
+__device__ __forceinline__ void put_words(char* rows, int stride, uint32_t n, uint32_t at, u32x4 x) {
+    const uint32_t token = at / (D / 2);
+    if (token >= n) x = u32x4{0u, 0u, 0u, 0u};
+    *reinterpret_cast<u32x4*>(rows + token * stride + 4 * (at % (D / 2))) = x;
+}
+template <int D, int T, int NV>
+__device__ __forceinline__ void put_raw_page(const u32x4* st, char* rows, int stride, uint32_t n) {
+    const uint32_t lane = lane_id();
+    if (n == (uint32_t)T) {
+#pragma unroll
+        for (int r = 0; r < NV; ++r) put_words<D>(rows, stride, T, 256u * r + 4u * lane, st[r]);
+    } else {
+#pragma unroll
+        for (int r = 0; r < NV; ++r) put_words<D>(rows, stride, n, 256u * r + 4u * lane, st[r]);
+    }
+}
+
+// A wave's 16 MR rows: queries, running maximum, sum and output, and the
+// scores of the TILES * 16 tokens at work.
+template <class E, int D, int MR, int TILES>
+struct Rows {
+    using V8 = typename E::V8;
+    static constexpr int DK = D / 32, DN = D / 16;
+    V8 q[MR][DK];
     float m[MR], l[MR];
     f32x4 o[MR][DN];
-    uint32_t q_row[MR];  // of lane's column; kNoPage past the last row
-    auto row_head = [&](uint32_t rho, uint32_t* j) __attribute__((always_inline)) {
-        const uint32_t i = rho / a.group;
-        *j = rho - i * a.group;
-        return first_row + i;
-    };
-    {
+    f32x4 s[MR][TILES];
+    uint32_t row[MR];  // of this lane's column in q and the mask; kNoPage past the last row
+
+    __device__ __forceinline__ void init(const AttnArgs& a, const Work& w, uint32_t row0) {
         const ArgsPtr c = args_again();
+        const uint32_t col = lane_id() & 15u, g = lane_id() >> 4;
 #pragma unroll
         for (int t = 0; t < MR; ++t) {
             const uint32_t rho = row0 + 16 * t + col;
-            uint32_t j;
-            q_row[t] = row_head(rho, &j);
-            if (rho >= rows) q_row[t] = kNoPage;
-            const uint16_t* qp = c->q + (int64_t)q_row[t] * c->q_row + (int64_t)(h * a.group + j) * c->q_head;
+            uint32_t head;
+            row[t] = row_of_group(a, w, rho, &head);
+            if (rho >= w.rows) row[t] = kNoPage;
+            const uint16_t* p = c->q + (int64_t)row[t] * c->q_row + (int64_t)head * c->q_head;
 #pragma unroll
             for (int kk = 0; kk < DK; ++kk) {
                 u32x4 x = {0u, 0u, 0u, 0u};
-                if (rho < rows) x = load_eight(qp + 32 * kk + 8 * g);
-                qf[t][kk] = bits_as<V8>(x ^ c->q_sign);  // (a negative scale is taken into the queries)
+                if (rho < w.rows) x = load_eight(p + 32 * kk + 8 * g);
+                q[t][kk] = bits_as<V8>(x ^ c->q_sign);  // (a negative scale is taken into the queries)
             }
             m[t] = -__builtin_inff();
             l[t] = 0.f;
@@ -332,50 +299,283 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
             for (int n = 0; n < DN; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
     }
-    // tables of the record formats, once the first pages are on their way
-    auto put_tables = [&]() __attribute__((always_inline)) {
-        if (4 * threadIdx.x < a.tab_words_k) reinterpret_cast<u32x4*>(smem)[threadIdx.x] = tab_k;
-        if (4 * threadIdx.x < a.tab_words_v) reinterpret_cast<u32x4*>(smem + a.tab_words_k)[threadIdx.x] = tab_v;
-        if (a.tab_words_k > 4 * kWave * kAttnWaves) stage_page_tables(a.k, smem, kWave * kAttnWaves);
-        if (a.tab_words_v > 4 * kWave * kAttnWaves) stage_page_tables(a.v, smem + a.tab_words_k, kWave * kAttnWaves);
+
+    // S^T = K Q^T
+    __device__ __forceinline__ void scores(const char* keys, int stride) {
+        const uint32_t col = lane_id() & 15u, g = lane_id() >> 4;
+#pragma unroll
+        for (int u = 0; u < TILES; ++u) {
+#pragma unroll
+            for (int t = 0; t < MR; ++t) s[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kk = 0; kk < DK; ++kk) {
+                const V8 kf = *reinterpret_cast<const V8*>(keys + (16 * u + col) * stride + 64 * kk + 16 * g);
+#pragma unroll
+                for (int t = 0; t < MR; ++t) s[t][u] = E::mfma(kf, q[t][kk], s[t][u]);
+            }
+        }
+    }
+
+    // Scores of row tile t, tile u that bit j of `seen` does not have: -infinity.
+    __device__ __forceinline__ void mask(int t, int u, uint32_t seen) {
+        const uint32_t g = lane_id() >> 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][u][e] = (seen >> (4 * g + e)) & 1u ? s[t][u][e] : -__builtin_inff();
+    }
+
+    // The running maximum and the weights, which take the scores' place.
+    __device__ __forceinline__ void weights(float scale2) {
+#pragma unroll
+        for (int t = 0; t < MR; ++t) {
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int u = 0; u < TILES; ++u) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, s[t][u][e]);
+            }
+            top = max_over_four(top) * scale2;
+            // The maximum is moved only when a score passes it by more than
+            // 8 (weights then stay below 2^8 and sums far from overflow), so
+            // most steps rescale nothing.
+            if (ballot(top > m[t] + 8.f || (m[t] == -__builtin_inff() && top != -__builtin_inff()))) {
+                const float m_new = fmaxf(m[t], top);
+                const float f = m_new == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(m[t] - m_new);
+                m[t] = m_new;
+                l[t] *= f;
+#pragma unroll
+                for (int n = 0; n < DN; ++n) o[t][n] *= f;
+            }
+            const float base = m[t] == -__builtin_inff() ? 0.f : -m[t];
+#pragma unroll
+            for (int u = 0; u < TILES; ++u) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[t][u][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][u][e], scale2, base));
+                l[t] += (s[t][u][0] + s[t][u][1]) + (s[t][u][2] + s[t][u][3]);
+            }
+        }
+    }
+
+    // O^T += V^T P^T
+    __device__ __forceinline__ void values(const char* vals, int stride) {
+        const uint32_t col = lane_id() & 15u, g = lane_id() >> 4;
+#pragma unroll
+        for (int u = 0; u < TILES; u += 2) {
+            V8 p[MR];
+#pragma unroll
+            for (int t = 0; t < MR; ++t) {
+                const u32x4 x = {E::pack(s[t][u][0], s[t][u][1]), E::pack(s[t][u][2], s[t][u][3]),
+                                 E::pack(s[t][u + 1][0], s[t][u + 1][1]), E::pack(s[t][u + 1][2], s[t][u + 1][3])};
+                p[t] = bits_as<V8>(x);
+            }
+            const char* at = vals + (16 * u + 4 * g + (col >> 2)) * stride + 8 * (col & 3);
+#pragma unroll
+            for (int n = 0; n < DN; ++n) {
+                const u32x2 x = read_transposed(at + 32 * n), y = read_transposed(at + 16 * stride + 32 * n);
+                const V8 vf = bits_as<V8>(u32x4{x[0], x[1], y[0], y[1]});
+#pragma unroll
+                for (int t = 0; t < MR; ++t) o[t][n] = E::mfma(vf, p[t], o[t][n]);
+            }
+        }
+    }
+};
+
+// Four dims of a row: the result, or this split's part of it.
+template <class E, int D>
+__device__ __forceinline__ void put_result(ArgsPtr c, uint32_t split, uint32_t row, uint32_t head, uint32_t d, f32x4 x,
+                                           float m, float l) {
+    const uint64_t rh = (uint64_t)row * (c->kv_heads * c->group) + head;
+    if (c->splits == 1) {
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        const u32x2 y = {E::pack(x[0] * inv, x[1] * inv), E::pack(x[2] * inv, x[3] * inv)};
+        *reinterpret_cast<u32x2*>(c->out + rh * D + d) = y;
+        if (d == 0 && c->lse)
+            c->lse[rh] = l > 0.f || l != l ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -__builtin_inff();
+    } else {
+        *reinterpret_cast<f32x4*>(c->part + (rh * c->splits + split) * D + d) = x;
+        if (d == 0) {
+            c->part_ml[(rh * c->splits + split) * 2] = m;
+            c->part_ml[(rh * c->splits + split) * 2 + 1] = l;
+        }
+    }
+}
+
+// Whole workgroup, after its results are in memory: drafted values j_lo ..
+// j_hi - 1 that are infinite or NaN, added to the rows that see them.  (They
+// were taken out of the products, where they would have reached every row
+// through a weight of zero.)
+template <class E, int D>
+__device__ __forceinline__ void add_odd_values(const AttnArgs& a, const Work& w, uint32_t rows_per_wg, uint32_t j_lo,
+                                               uint32_t j_hi) {
+    const ArgsPtr c = args_again();
+    const uint32_t n_rows = min(w.rows - w.rt * rows_per_wg, rows_per_wg);
+#pragma unroll 1
+    for (uint32_t e = threadIdx.x; e < n_rows * D; e += blockDim.x) {
+        const uint32_t d = e % D;
+        uint32_t head;
+        const uint32_t row = row_of_group(a, w, w.rt * rows_per_wg + e / D, &head);
+        float sum = 0.f;
+        bool any = false;
+#pragma unroll 1
+        for (uint32_t k = j_lo; k < j_hi; ++k) {
+            if (!((c->mask[(uint64_t)row * c->mask_words2 + k / 32] >> (k % 32)) & 1u)) continue;
+            const uint32_t v = c->v_new[(int64_t)(w.first_row + k) * c->new_row + (int64_t)w.h * c->new_head + d];
+            if ((v & E::kExponent) != E::kExponent) continue;
+            sum += E::from_bits(v);
+            any = true;
+        }
+        if (!any) continue;
+        const uint64_t rh = (uint64_t)row * (c->kv_heads * c->group) + head;
+        if (c->splits == 1)
+            c->out[rh * D + d] = (uint16_t)E::pack(E::from_bits(c->out[rh * D + d]) + sum, 0.f);
+        else
+            c->part[(rh * c->splits + w.split) * D + d] += sum;
+    }
+}
+
+// The step that covers tokens 0 .. n - 1 of 16 TILES from its first: bit j of
+// tile u's tokens.
+__device__ __forceinline__ uint32_t tile_bits(uint32_t n, int u) {
+    const uint32_t k = n > 16u * u ? n - 16u * u : 0u;
+    return k >= 16u ? 0xFFFFu : (1u << k) - 1u;
+}
+
+// Mask words of drafted tokens 32 word .. for a lane's rows.
+template <int MR, int WORDS>
+__device__ __forceinline__ void load_sees(uint32_t (&sees)[MR][WORDS], const uint32_t (&row)[MR], uint32_t word) {
+    const ArgsPtr c = args_again();
+#pragma unroll
+    for (int t = 0; t < MR; ++t) {
+#pragma unroll
+        for (int x = 0; x < WORDS; ++x) {
+            sees[t][x] = 0;
+            if (row[t] != kNoPage && word + x < c->mask_words2)
+                sees[t][x] = c->mask[(uint64_t)row[t] * c->mask_words2 + word + x];
+        }
+    }
+}
+
+template <class E, int D, int T, int MR, bool TREE>
+__global__ __launch_bounds__(kWave * kFewWaves, 2) void k_attend_few(AttnArgs a) {
+    using S = FewShape<D, T>;
+    constexpr int NV = S::NV, STEP = S::STEP, PW = S::PW, TILES = STEP / 16, DN = D / 16;
+    constexpr uint32_t kRowsWg = 16u * MR;
+    extern __shared__ __align__(16) uint32_t smem[];
+    __shared__ float join_m[kFewWaves][16], join_l[kFewWaves][16];
+    __shared__ uint32_t odd_values;  // an infinity or NaN among the drafted values
+    const uint32_t lane = lane_id(), wib = uniform(threadIdx.x / kWave);
+    const uint32_t col = lane & 15u, g = lane >> 4;
+
+    EarlyTables tables;
+    tables.load(a);
+    if (TREE && threadIdx.x == 0) odd_values = 0;
+    Work w;
+    if (!find_work<T, TREE>(a, kRowsWg, w)) return;
+    const uint32_t row0 = w.rt * kRowsWg;
+
+    // steps of this split: the context's, then the drafted tokens'
+    const uint32_t ctx_pages = TREE ? ((uint32_t)w.len + T - 1) / T : (w.len > 0 ? a.n_list : 0u);
+    const uint32_t ctx_steps = (ctx_pages + PW - 1) / PW;
+    const uint32_t all_steps = ctx_steps + (TREE ? (w.n_new + STEP - 1) / STEP : 0u);
+    const uint32_t per = (all_steps + a.splits - 1) / a.splits;
+    const uint32_t s_lo = min(w.split * per, all_steps), s_hi = min(s_lo + per, all_steps);
+    const uint32_t s_first = s_lo + wib;
+    const uint32_t n_steps = s_first < s_hi ? (s_hi - s_first + kFewWaves - 1) / kFewWaves : 0u;
+
+    char* const area = reinterpret_cast<char*>(smem + a.tab_words_k + a.tab_words_v);
+    uint32_t* const stage = reinterpret_cast<uint32_t*>(area + wib * S::wave_bytes);
+    char* const tile = reinterpret_cast<char*>(stage) + PW * S::stage_bytes;  // keys, then values
+
+    Rows<E, D, MR, TILES> rows;
+    rows.init(a, w, row0);
+
+    // --- the wave's next pages: lane l has page l % PW of its step base + l / PW
+    uint32_t id_k = 0, id_v = 0, held = 0, comp = 0;
+    auto refill = [&](uint32_t base) __attribute__((always_inline)) {
+        const ArgsPtr c = args_again();
+        const uint32_t s = s_first + (base + lane / PW) * kFewWaves;
+        id_k = id_v = held = comp = 0;
+        if (s < s_hi && s < ctx_steps) {
+            const uint32_t n = s * PW + lane % PW;
+            int32_t block = n < ctx_pages ? (int32_t)n : -1;
+            if (!TREE && n < ctx_pages) block = c->blocks[((uint64_t)w.item * a.kv_heads + w.h) * c->n_list + n];
+            if (block >= 0 && (int64_t)block * T < w.len) {
+                held = (uint32_t)min(T, w.len - block * T);
+                const uint64_t at = ((uint64_t)w.seq * a.kv_heads + w.h) * c->table_blocks + (uint32_t)block;
+                // both ids, then both bits, each pair in one latency
+                const int64_t k64 = c->k_table[at], v64 = c->v_table[at];
+                const uint32_t k = page_id(k64, c->k.n_slots), v = page_id(v64, c->v.n_slots);
+                id_k = k == kNoPage ? 0u : k;
+                id_v = v == kNoPage ? 0u : v;
+                const uint32_t k_word = c->k.bitmask[id_k >> 5], v_word = c->v.bitmask[id_v >> 5];
+                comp = (k == kNoPage ? 0u : (k_word >> (id_k & 31u)) & 1u) |
+                       (v == kNoPage ? 0u : ((v_word >> (id_v & 31u)) & 1u) << 1);
+                if (k == kNoPage || v == kNoPage) atomicCAS(c->k.err, 0u, (uint32_t)kErrRange);
+            }
+        }
+    };
+    auto load = [&](u32x4* st, uint32_t j, bool values, uint32_t ids) __attribute__((always_inline)) {
+        const uint32_t s = s_first + j * kFewWaves;
+#pragma unroll
+        for (int p = 0; p < PW; ++p) {
+            if (!TREE || s < ctx_steps)
+                load_page<NV>(st + p * NV, values ? a.v.slots : a.k.slots,
+                              lane_value(ids, (int)((j % (64 / PW)) * PW + p)));
+            else
+                load_drafted<D, NV>(st + p * NV, w, values, (s - ctx_steps) * STEP + p * T);
+        }
+    };
+    // The wave's pages as rows of tokens in LDS.  A record goes through the
+    // stage; values behind a page's last token become zero.
+    auto put = [&](const u32x4* st, bool values, uint32_t records, const uint32_t* keep) __attribute__((
+                   always_inline)) {
+        const int stride = values ? S::RV : S::RK;
+        lds_order();
+#pragma unroll
+        for (int p = 0; p < PW; ++p) {
+            if ((records >> p) & 1u)
+                stage_page<NV>(st + p * NV, stage + p * (S::stage_bytes / 4));
+            else
+                put_raw_page<D, T, NV>(st + p * NV, tile + p * T * stride, stride, values ? keep[p] : (uint32_t)T);
+        }
+        for (; records; records &= records - 1) {
+            const uint32_t p = PW == 1 ? 0u : (uint32_t)__builtin_ctz(records);
+            const uint32_t n = !values ? (uint32_t)T : PW == 1 || p == 0 ? keep[0] : keep[PW - 1];
+            if (!rebuild_page<NV, S::U>(values ? a.v : a.k, kind_tab(a, smem, values),
+                                        stage + p * (S::stage_bytes / 4),
+                                        [&](uint32_t at, u32x4 x) __attribute__((always_inline)) {
+                                            put_words<D>(tile + p * T * stride, stride, n, at, x);
+                                        }))
+                latch_error(args_again()->k.err, kErrCorrupt);
+        }
+        lds_order();
     };
 
-    u32x4 st_a[PW * NV], st_b[S::BOTH && !S::ONE ? PW * NV : 1];
+    u32x4 st_a[PW * NV], st_b[S::ONE ? 1 : PW * NV];
     bool odd = false;
-    // of the step at work and of the next: tokens of each page that the wave
-    // loads, and the rows' mask words of drafted steps; which pages at work
-    // are records (keys, then values); ids of the value pages at work (ONE)
-    uint32_t n_held[PW], next_held[PW], records = 0, ids_b = 0;
-    uint32_t sees[TREE ? MR : 1][STEP / 32], next_sees[TREE ? MR : 1][STEP / 32];
+    // of the step at work and of the next: tokens of each page, and the rows'
+    // mask words of drafted steps; which pages at work are records (keys, then
+    // values); ids of the value pages at work (ONE)
+    uint32_t n_held[PW], next_held[PW], records = 0, ids_v = 0;
+    uint32_t sees[MR][STEP / 32], next_sees[MR][STEP / 32];
     auto facts = [&](uint32_t j) __attribute__((always_inline)) {
-        const uint32_t sn = s_first + j * kStride;
+        const uint32_t sn = s_first + j * kFewWaves;
+        const bool drafted = TREE && sn >= ctx_steps;
 #pragma unroll
         for (int p = 0; p < PW; ++p) {
             next_held[p] = lane_value(held, (int)((j % (64 / PW)) * PW + p));
-            if (TREE && sn >= ctx_steps) {
-                const uint32_t j0 = (sn - ctx_steps) * STEP + (SHARED ? page_in_step : (uint32_t)p) * T;
-                next_held[p] = n_new > j0 ? min(n_new - j0, (uint32_t)T) : 0u;
+            if (drafted) {
+                const uint32_t j0 = (sn - ctx_steps) * STEP + p * T;
+                next_held[p] = w.n_new > j0 ? min(w.n_new - j0, (uint32_t)T) : 0u;
             }
         }
-        if (TREE && sn >= ctx_steps) {
-            const ArgsPtr x = args_again();
-#pragma unroll
-            for (int t = 0; t < MR; ++t) {
-#pragma unroll
-                for (int w = 0; w < STEP / 32; ++w) {
-                    const uint32_t word = (sn - ctx_steps) * (STEP / 32) + w;
-                    next_sees[t][w] = 0;
-                    if (q_row[t] != kNoPage && word < x->mask_words2)
-                        next_sees[t][w] = x->mask[(uint64_t)q_row[t] * x->mask_words2 + word];
-                }
-            }
-        }
+        if (drafted) load_sees(next_sees, rows.row, (sn - ctx_steps) * (STEP / 32));
     };
     // step j becomes the one at work (after its loads have been sent: the
     // records' bits come a latency after the ids)
     auto advance = [&](uint32_t j) __attribute__((always_inline)) {
         records = 0;
-        ids_b = id_b;
+        ids_v = id_v;
 #pragma unroll
         for (int p = 0; p < PW; ++p) {
             n_held[p] = next_held[p];
@@ -388,288 +588,271 @@ __global__ __launch_bounds__(kWave * kAttnWaves, 2) void k_attend(AttnArgs a) {
 #pragma unroll
             for (int t = 0; t < MR; ++t) {
 #pragma unroll
-                for (int w = 0; w < STEP / 32; ++w) sees[t][w] = next_sees[t][w];
-            }
-        }
-    };
-#pragma unroll
-    for (int t = 0; t < (TREE ? MR : 1); ++t) {
-#pragma unroll
-        for (int w = 0; w < STEP / 32; ++w) sees[t][w] = next_sees[t][w] = 0;
-    }
-    if (n_steps) {
-        refill(0);
-        facts(0);
-        load(st_a, 0, only_v, id_a);
-        if constexpr (S::BOTH && !S::ONE) load(st_b, 0, true, id_b);
-    }
-    put_tables();
-    if (n_steps) {
-        advance(0);
-        take_sees();
-    }
-    if constexpr (!SHARED) __syncthreads();  // (the loop of SHARED begins with one)
-
-    for (uint32_t i = 0; i < n_steps; ++i) {
-        const bool more = i + 1 < n_steps;
-        const uint32_t s = s_first + i * kStride;
-        const bool draft = TREE && s >= ctx_steps;
-        auto put_keys = [&]() __attribute__((always_inline)) {
-            put(st_a, false, records & ((1u << PW) - 1), n_held, k_tile, S::RK);
-        };
-        auto put_values = [&](u32x4* st, uint32_t shift) __attribute__((always_inline)) {
-            // Infinities and NaNs of drafted values are taken out, so that
-            // they reach no row through a product with a weight of zero, and
-            // added at the end to the rows that see them.
-            if (draft) {
-#pragma unroll
-                for (int r = 0; r < PW * NV; ++r) odd |= clear_odd<E>(st[r]);
-            }
-            put(st, true, records >> shift, n_held, v_tile, S::RV);
-        };
-        if constexpr (SHARED) {
-            __syncthreads();  // the tiles are free, and the tables there
-            if (S::BOTH) {
-                put_keys();
-                put_values(st_b, PW);
-            } else if (only_v) {
-                put_values(st_a, 0);
-            } else {
-                put_keys();
-            }
-        } else {
-            put_keys();
-        }
-        const uint32_t step_held_all =
-            draft ? min(n_new - (s - ctx_steps) * STEP, (uint32_t)STEP) : min((uint32_t)len - s * STEP, (uint32_t)STEP);
-        uint32_t tiles_held[!TREE && !SHARED ? PW : 1];  // tokens of the pages at work, for the masks
-        if constexpr (!TREE && !SHARED) {
-#pragma unroll
-            for (int p = 0; p < PW; ++p) tiles_held[p] = n_held[p];
-        }
-        if constexpr (S::ONE) load(st_a, i, true, ids_b);
-        if (more) {
-            if ((i + 1) % (64 / PW) == 0) refill(i + 1);
-            facts(i + 1);
-            if constexpr (!S::ONE) load(st_a, i + 1, only_v, id_a);
-            if constexpr (SHARED && S::BOTH) load(st_b, i + 1, true, id_b);
-        }
-        if constexpr (SHARED) {
-            if (more) advance(i + 1);
-            __syncthreads();
-        }
-#pragma unroll 1
-        for (uint32_t c = 0; c < (uint32_t)(STEP / S::CHUNK); ++c) {
-            // valid tokens of each tile of 16
-            const uint32_t t0 = c * S::CHUNK;
-            auto tile_held = [&](int u) __attribute__((always_inline)) -> uint32_t {
-                if constexpr (TREE || SHARED) {
-                    const uint32_t before = t0 + 16u * u;
-                    return step_held_all > before ? step_held_all - before : 0u;
-                } else {
-                    const uint32_t n = tiles_held[(u * 16) / T < PW ? (u * 16) / T : 0];
-                    return n > (uint32_t)(u * 16 % T) ? n - (uint32_t)(u * 16 % T) : 0u;
-                }
-            };
-            const char* const kt = k_tile + t0 * S::RK;
-            const char* const vt = v_tile + t0 * S::RV;
-            // S^T = K Q^T
-            f32x4 sc[MR][TILES];
-#pragma unroll
-            for (int u = 0; u < TILES; ++u) {
-#pragma unroll
-                for (int t = 0; t < MR; ++t) sc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kk = 0; kk < DK; ++kk) {
-                    const V8 kf = *reinterpret_cast<const V8*>(kt + (16 * u + col) * S::RK + 64 * kk + 16 * g);
-#pragma unroll
-                    for (int t = 0; t < MR; ++t) sc[t][u] = E::mfma(kf, qf[t][kk], sc[t][u]);
-                }
-            }
-            // masked scores -infinity, the running maximum, weights
-            bool whole = !draft;
-#pragma unroll
-            for (int u = 0; u < TILES; ++u) whole = whole && tile_held(u) >= 16u;
-            if (!whole) {
-#pragma unroll
-                for (int t = 0; t < MR; ++t) {
-#pragma unroll
-                    for (int u = 0; u < TILES; ++u) {
-                        // bit j of `seen`: the lane's row sees token j of the tile
-                        uint32_t seen = tile_held(u) >= 16u ? 0xFFFFu : (1u << tile_held(u)) - 1u;
-                        if (draft) {
-                            uint32_t bits = sees[TREE ? t : 0][u / 2];
-                            if constexpr (STEP > S::CHUNK) bits = c ? sees[TREE ? t : 0][STEP / 64 + u / 2] : bits;
-                            seen &= bits >> (16 * (u & 1));
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            sc[t][u][e] = (seen >> (4 * g + e)) & 1u ? sc[t][u][e] : -__builtin_inff();
-                    }
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < MR; ++t) {
-                float top = -__builtin_inff();
-#pragma unroll
-                for (int u = 0; u < TILES; ++u) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[t][u][e]);
-                }
-                top = max_over_four(top) * a.scale2;
-                // The maximum is moved only when a score passes it by more
-                // than 8 (weights then stay below 2^8 and sums far from
-                // overflow), so most steps rescale nothing.
-                if (ballot(top > m[t] + 8.f || (m[t] == -__builtin_inff() && top != -__builtin_inff()))) {
-                    const float m_new = fmaxf(m[t], top);
-                    const float f = m_new == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(m[t] - m_new);
-                    m[t] = m_new;
-                    l[t] *= f;
-#pragma unroll
-                    for (int n = 0; n < DN; ++n) o[t][n] *= f;
-                }
-                const float base = m[t] == -__builtin_inff() ? 0.f : -m[t];
-#pragma unroll
-                for (int u = 0; u < TILES; ++u) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][u][e], a.scale2, base));
-                        sc[t][u][e] = p;
-                    }
-                    l[t] += (sc[t][u][0] + sc[t][u][1]) + (sc[t][u][2] + sc[t][u][3]);
-                }
-            }
-
-            if constexpr (!SHARED) put_values(S::ONE ? st_a : st_b, PW);
-            if constexpr (!SHARED) {
-                if (more) {
-                    if constexpr (S::ONE)
-                        load(st_a, i + 1, false, id_a);
-                    else
-                        load(st_b, i + 1, true, id_b);
-                    advance(i + 1);
-                }
-            }
-            // O^T += V^T P^T
-#pragma unroll
-            for (int u = 0; u < TILES; u += 2) {
-                V8 pf[MR];
-#pragma unroll
-                for (int t = 0; t < MR; ++t) {
-                    const u32x4 x = {E::pack(sc[t][u][0], sc[t][u][1]), E::pack(sc[t][u][2], sc[t][u][3]),
-                                     E::pack(sc[t][u + 1][0], sc[t][u + 1][1]),
-                                     E::pack(sc[t][u + 1][2], sc[t][u + 1][3])};
-                    pf[t] = bits_as<V8>(x);
-                }
-                const char* vp = vt + (16 * u + 4 * g + (col >> 2)) * S::RV + 8 * (col & 3);
-#pragma unroll
-                for (int n = 0; n < DN; ++n) {
-                    const u32x2 x = read_transposed(vp + 32 * n), y = read_transposed(vp + 16 * S::RV + 32 * n);
-                    const V8 vf = bits_as<V8>(u32x4{x[0], x[1], y[0], y[1]});
-#pragma unroll
-                    for (int t = 0; t < MR; ++t) o[t][n] = E::mfma(vf, pf[t], o[t][n]);
-                }
-            }
-            lds_order();
-        }
-        if (more) take_sees();
-    }
-
-    // --- the sums over the four lanes of a row, then the result or this split's part
-    const ArgsPtr c = args_again();
-    const uint32_t nq = c->kv_heads * c->group, splits = c->splits;
-    auto finish = [&](uint32_t row, uint32_t head, uint32_t d, f32x4 x, float mm, float ll) __attribute__((
-                      always_inline)) {
-        const uint64_t rh = (uint64_t)row * nq + head;
-        if (splits == 1) {
-            const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
-            const u32x2 y = {E::pack(x[0] * inv, x[1] * inv), E::pack(x[2] * inv, x[3] * inv)};
-            *reinterpret_cast<u32x2*>(c->out + rh * D + d) = y;
-            if (d == 0 && c->lse)
-                c->lse[rh] = ll > 0.f || ll != ll ? (mm + __builtin_amdgcn_logf(ll)) * kLn2 : -__builtin_inff();
-        } else {
-            *reinterpret_cast<f32x4*>(c->part + (rh * splits + split) * D + d) = x;
-            if (d == 0) {
-                c->part_ml[(rh * splits + split) * 2] = mm;
-                c->part_ml[(rh * splits + split) * 2 + 1] = ll;
+                for (int x = 0; x < STEP / 32; ++x) sees[t][x] = next_sees[t][x];
             }
         }
     };
 #pragma unroll
     for (int t = 0; t < MR; ++t) {
-        l[t] = sum_over_four(l[t]);
-        if constexpr (SHARED) {
-            uint32_t j;
-            const uint32_t row = row_head(row0 + 16 * t + col, &j);
-            if (q_row[t] != kNoPage) {
 #pragma unroll
-                for (int n = 0; n < DN; ++n) finish(row, h * a.group + j, 16 * n + 4 * g, o[t][n], m[t], l[t]);
-            }
-        } else {
-            // the waves' rows joined through LDS: [wave][row][D + 4]
-            float* const buf = reinterpret_cast<float*>(area);
-            __syncthreads();
+        for (int x = 0; x < STEP / 32; ++x) sees[t][x] = next_sees[t][x] = 0;
+    }
+    if (n_steps) {
+        refill(0);
+        facts(0);
+        load(st_a, 0, false, id_k);
+        if constexpr (!S::ONE) load(st_b, 0, true, id_v);
+    }
+    tables.put(a, smem);
+    if (n_steps) {
+        advance(0);
+        take_sees();
+    }
+    __syncthreads();
+
+    for (uint32_t i = 0; i < n_steps; ++i) {
+        const bool more = i + 1 < n_steps;
+        const uint32_t s = s_first + i * kFewWaves;
+        const bool draft = TREE && s >= ctx_steps;
+        put(st_a, false, records & ((1u << PW) - 1), n_held);
+        uint32_t tokens[PW];  // of the pages at work, for the masks
+        bool whole = !draft;
 #pragma unroll
-            for (int n = 0; n < DN; ++n)
-                *reinterpret_cast<f32x4*>(buf + (wib * 16 + col) * (D + 4) + 16 * n + 4 * g) = o[t][n];
-            if (g == 0) {
-                join_m[wib][col] = m[t];
-                join_l[wib][col] = l[t];
-            }
-            __syncthreads();
-#pragma unroll 1
-            for (uint32_t e = threadIdx.x; e < 16 * (D / 4); e += kWave * kAttnWaves) {
-                const uint32_t cc = e / (D / 4), d = 4 * (e % (D / 4));
-                const uint32_t rho = row0 + 16 * t + cc;
-                if (rho >= rows) break;
-                float mm = -__builtin_inff(), ll = 0.f;
+        for (int p = 0; p < PW; ++p) {
+            tokens[p] = n_held[p];
+            whole = whole && n_held[p] == (uint32_t)T;
+        }
+        if constexpr (S::ONE) load(st_a, i, true, ids_v);
+        if (more) {
+            if ((i + 1) % (64 / PW) == 0) refill(i + 1);
+            facts(i + 1);
+            if constexpr (!S::ONE) load(st_a, i + 1, false, id_k);
+        }
+        rows.scores(tile, S::RK);
+        if (!whole) {
 #pragma unroll
-                for (uint32_t w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, join_m[w][cc]);
-                const float base = mm == -__builtin_inff() ? 0.f : mm;
-                f32x4 x = {0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < MR; ++t) {
 #pragma unroll
-                for (uint32_t w = 0; w < kAttnWaves; ++w) {
-                    const float f = __builtin_amdgcn_exp2f(join_m[w][cc] - base);
-                    ll += f * join_l[w][cc];
-                    x += f * *reinterpret_cast<const f32x4*>(buf + (w * 16 + cc) * (D + 4) + d);
+                for (int u = 0; u < TILES; ++u) {
+                    uint32_t seen = tile_bits(tokens[16 * u / T], u - 16 * u / T * (T / 16));
+                    if (draft) seen &= sees[t][u / 2] >> (16 * (u & 1));
+                    rows.mask(t, u, seen);
                 }
-                uint32_t j;
-                const uint32_t row = row_head(rho, &j);
-                finish(row, h * a.group + j, d, x, mm, ll);
             }
+        }
+        rows.weights(a.scale2);
+        u32x4* const st_v = S::ONE ? st_a : st_b;
+        if (draft) {
+#pragma unroll
+            for (int r = 0; r < PW * NV; ++r) odd |= clear_odd<E>(st_v[r]);
+        }
+        put(st_v, true, records >> PW, n_held);
+        if (more) {
+            if constexpr (S::ONE)
+                load(st_a, i + 1, false, id_k);
+            else
+                load(st_b, i + 1, true, id_v);
+            advance(i + 1);
+        }
+        rows.values(tile, S::RV);
+        lds_order();
+        if (more) take_sees();
+    }
+
+    // --- the waves' rows joined through LDS: [wave][row][D + 4]
+    const ArgsPtr c = args_again();
+#pragma unroll
+    for (int t = 0; t < MR; ++t) {
+        const float l = sum_over_four(rows.l[t]);
+        float* const buf = reinterpret_cast<float*>(area);
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < DN; ++n)
+            *reinterpret_cast<f32x4*>(buf + (wib * 16 + col) * (D + 4) + 16 * n + 4 * g) = rows.o[t][n];
+        if (g == 0) {
+            join_m[wib][col] = rows.m[t];
+            join_l[wib][col] = l;
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (uint32_t e = threadIdx.x; e < 16 * (D / 4); e += kWave * kFewWaves) {
+            const uint32_t r = e / (D / 4), d = 4 * (e % (D / 4));
+            const uint32_t rho = row0 + 16 * t + r;
+            if (rho >= w.rows) break;
+            float mm = -__builtin_inff(), ll = 0.f;
+#pragma unroll
+            for (uint32_t v = 0; v < kFewWaves; ++v) mm = fmaxf(mm, join_m[v][r]);
+            const float base = mm == -__builtin_inff() ? 0.f : mm;
+            f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (uint32_t v = 0; v < kFewWaves; ++v) {
+                const float f = __builtin_amdgcn_exp2f(join_m[v][r] - base);
+                ll += f * join_l[v][r];
+                x += f * *reinterpret_cast<const f32x4*>(buf + (v * 16 + r) * (D + 4) + d);
+            }
+            uint32_t head;
+            const uint32_t row = row_of_group(a, w, rho, &head);
+            put_result<E, D>(c, w.split, row, head, d, x, mm, ll);
         }
     }
     if constexpr (TREE) {
-        // Drafted values that are infinite or NaN: added to what the rows
-        // that see them have in memory.
         if (ballot(odd) && lane == 0) odd_values = 1;
         __syncthreads();
-        if (odd_values) {
-            const uint32_t j_lo = s_lo > ctx_steps ? (s_lo - ctx_steps) * STEP : 0u;
-            const uint32_t j_hi = s_hi > ctx_steps ? min((s_hi - ctx_steps) * STEP, n_new) : 0u;
-            const uint32_t n_rows = min(rows - rt * kRowsWg, kRowsWg);
-            for (uint32_t e = threadIdx.x; e < n_rows * D; e += kWave * kAttnWaves) {
-                const uint32_t d = e % D;
-                uint32_t j;
-                const uint32_t row = row_head(rt * kRowsWg + e / D, &j);
-                float sum = 0.f;
-                bool any = false;
-                for (uint32_t k = j_lo; k < j_hi; ++k) {
-                    if (!((c->mask[(uint64_t)row * c->mask_words2 + k / 32] >> (k % 32)) & 1u)) continue;
-                    const uint32_t v = c->v_new[(int64_t)(first_row + k) * c->new_row + (int64_t)h * c->new_head + d];
-                    if ((v & E::kExponent) != E::kExponent) continue;
-                    sum += E::from_bits(v);
-                    any = true;
-                }
-                if (!any) continue;
-                const uint64_t rh = (uint64_t)row * nq + h * a.group + j;
-                if (splits == 1)
-                    c->out[rh * D + d] = (uint16_t)E::pack(E::from_bits(c->out[rh * D + d]) + sum, 0.f);
+        if (odd_values)
+            add_odd_values<E, D>(a, w, kRowsWg, s_lo > ctx_steps ? (s_lo - ctx_steps) * STEP : 0u,
+                                 s_hi > ctx_steps ? min((s_hi - ctx_steps) * STEP, w.n_new) : 0u);
+    }
+}
+
+template <class E, int D, int T, int MR>
+__global__ __launch_bounds__(kWave * kManyWaves, 2) void k_attend_many(AttnArgs a) {
+    using S = ManyShape<D, T>;
+    constexpr int NV = S::NV, STEP = S::STEP, TILES = STEP / 16, DN = D / 16;
+    constexpr uint32_t kRowsWg = 16u * MR * kManyWaves;
+    extern __shared__ __align__(16) uint32_t smem[];
+    __shared__ uint32_t odd_values;  // an infinity or NaN among the drafted values
+    const uint32_t lane = lane_id(), wib = uniform(threadIdx.x / kWave);
+    const uint32_t col = lane & 15u, g = lane >> 4;
+
+    EarlyTables tables;
+    tables.load(a);
+    if (threadIdx.x == 0) odd_values = 0;
+    Work w;
+    if (!find_work<T, true>(a, kRowsWg, w)) return;
+
+    const uint32_t ctx_steps = ((uint32_t)w.len + STEP - 1) / STEP;
+    const uint32_t all_steps = ctx_steps + (w.n_new + STEP - 1) / STEP;
+    const uint32_t per = (all_steps + a.splits - 1) / a.splits;
+    const uint32_t s_lo = min(w.split * per, all_steps), s_hi = min(s_lo + per, all_steps);
+
+    // this wave's page of every ROUNDS-th step: of keys and values, or of one
+    const uint32_t job = wib % S::JOBS, phase = wib / S::JOBS;
+    const bool only_v = !S::BOTH && job >= (uint32_t)S::KP;
+    const uint32_t page = only_v ? job - S::KP : job;
+    char* const area = reinterpret_cast<char*>(smem + a.tab_words_k + a.tab_words_v);
+    uint32_t* const stage = reinterpret_cast<uint32_t*>(area + S::tile_bytes + job * S::stage_bytes);
+
+    // lane l: ids and bits (keys, then values) of the wave's page of its own
+    // step base + l
+    uint32_t id_k = 0, id_v = 0, comp = 0;
+    auto refill = [&](uint32_t base) __attribute__((always_inline)) {
+        const ArgsPtr c = args_again();
+        const uint32_t s = s_lo + phase + (base + lane) * S::ROUNDS;
+        const uint32_t block = s * S::KP + page;
+        id_k = id_v = comp = 0;
+        if (s < s_hi && s < ctx_steps && block * T < (uint32_t)w.len) {
+            const uint64_t at = ((uint64_t)w.seq * a.kv_heads + w.h) * c->table_blocks + block;
+            // both ids, then both bits, each pair in one latency
+            const int64_t k64 = c->k_table[at], v64 = c->v_table[at];
+            const uint32_t k = page_id(k64, c->k.n_slots), v = page_id(v64, c->v.n_slots);
+            id_k = k == kNoPage ? 0u : k;
+            id_v = v == kNoPage ? 0u : v;
+            const uint32_t k_word = c->k.bitmask[id_k >> 5], v_word = c->v.bitmask[id_v >> 5];
+            comp = (k == kNoPage ? 0u : (k_word >> (id_k & 31u)) & 1u) |
+                   (v == kNoPage ? 0u : ((v_word >> (id_v & 31u)) & 1u) << 1);
+            if (k == kNoPage || v == kNoPage) atomicCAS(c->k.err, 0u, (uint32_t)kErrRange);
+        }
+    };
+    u32x4 st_a[NV], st_b[S::BOTH ? NV : 1];
+    bool odd = false;
+    uint32_t k = 0;  // own steps loaded so far
+    auto load = [&]() __attribute__((always_inline)) {
+        const uint32_t s = s_lo + phase + k * S::ROUNDS;
+        if (s >= s_hi) return;
+        if (k % 64 == 0) refill(k);
+        if (s < ctx_steps) {
+            load_page<NV>(st_a, only_v ? a.v.slots : a.k.slots, lane_value(only_v ? id_v : id_k, (int)(k % 64)));
+            if constexpr (S::BOTH) load_page<NV>(st_b, a.v.slots, lane_value(id_v, (int)(k % 64)));
+        } else {
+            load_drafted<D, NV>(st_a, w, only_v, (s - ctx_steps) * STEP + page * T);
+            if constexpr (S::BOTH) load_drafted<D, NV>(st_b, w, true, (s - ctx_steps) * STEP + page * T);
+        }
+        ++k;
+    };
+    // a page of step s to its rows of tokens in LDS; values behind the last
+    // token become zero
+    auto put = [&](u32x4* st, bool values, uint32_t s) __attribute__((always_inline)) {
+        const int stride = values ? S::RV : S::RK;
+        char* const to = area + (values ? STEP * S::RK : 0) + page * T * stride;
+        const bool drafted = s >= ctx_steps;
+        const uint32_t first = (drafted ? s - ctx_steps : s) * STEP + page * T;
+        const uint32_t end = drafted ? w.n_new : (uint32_t)w.len;
+        const uint32_t held = !values ? (uint32_t)T : end > first ? min(end - first, (uint32_t)T) : 0u;
+        if (drafted && values) {
+#pragma unroll
+            for (int r = 0; r < NV; ++r) odd |= clear_odd<E>(st[r]);
+        }
+        lds_order();
+        if (!drafted && ((lane_value(comp, (int)((k - 1) % 64)) >> (values ? 1 : 0)) & 1u)) {
+            stage_page<NV>(st, stage);
+            if (!rebuild_page<NV, S::U>(values ? a.v : a.k, kind_tab(a, smem, values), stage,
+                                        [&](uint32_t at, u32x4 x) __attribute__((always_inline)) {
+                                            put_words<D>(to, stride, held, at, x);
+                                        }))
+                latch_error(args_again()->k.err, kErrCorrupt);
+        } else {
+            put_raw_page<D, T, NV>(st, to, stride, held);
+        }
+        lds_order();
+    };
+
+    load();
+    Rows<E, D, MR, TILES> rows;
+    rows.init(a, w, w.rt * kRowsWg + wib * 16u * MR);
+    tables.put(a, smem);
+
+    for (uint32_t s = s_lo; s < s_hi; ++s) {
+        const bool draft = s >= ctx_steps;
+        uint32_t sees[MR][STEP / 32];
+        if (draft) load_sees(sees, rows.row, (s - ctx_steps) * (STEP / 32));
+        __syncthreads();  // the tiles are free, and the tables there
+        if (S::ROUNDS == 1 || (s - s_lo) % S::ROUNDS == phase) {
+            if constexpr (S::BOTH) {
+                put(st_a, false, s);
+                put(st_b, true, s);
+            } else {
+                if (only_v)
+                    put(st_a, true, s);
                 else
-                    c->part[(rh * splits + split) * D + d] += sum;
+                    put(st_a, false, s);
+            }
+            load();
+        }
+        __syncthreads();
+        const uint32_t tokens = draft ? w.n_new - (s - ctx_steps) * STEP : (uint32_t)w.len - s * STEP;
+        rows.scores(area, S::RK);
+        if (draft || tokens < (uint32_t)STEP) {
+#pragma unroll
+            for (int t = 0; t < MR; ++t) {
+#pragma unroll
+                for (int u = 0; u < TILES; ++u) {
+                    uint32_t seen = tile_bits(tokens, u);
+                    if (draft) seen &= sees[t][u / 2] >> (16 * (u & 1));
+                    rows.mask(t, u, seen);
+                }
             }
         }
+        rows.weights(a.scale2);
+        rows.values(area + STEP * S::RK, S::RV);
     }
+
+    const ArgsPtr c = args_again();
+#pragma unroll
+    for (int t = 0; t < MR; ++t) {
+        const float l = sum_over_four(rows.l[t]);
+        uint32_t head;
+        const uint32_t row = row_of_group(a, w, w.rt * kRowsWg + (wib * MR + t) * 16u + col, &head);
+        if (rows.row[t] != kNoPage) {
+#pragma unroll
+            for (int n = 0; n < DN; ++n)
+                put_result<E, D>(c, w.split, row, head, 16 * n + 4 * g, rows.o[t][n], rows.m[t], l);
+        }
+    }
+    if (ballot(odd) && lane == 0) odd_values = 1;
+    __syncthreads();
+    if (odd_values)
+        add_odd_values<E, D>(a, w, kRowsWg, s_lo > ctx_steps ? (s_lo - ctx_steps) * STEP : 0u,
+                             s_hi > ctx_steps ? min((s_hi - ctx_steps) * STEP, w.n_new) : 0u);
 }
 
 // The splits' parts joined: D / 4 lanes per (row, head).
@@ -706,7 +889,7 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a) {
 // Shape of a launch, chosen by the host (plan_attention).
 struct AttnPlan {
     int mr = 1;              // tiles of 16 rows per wave
-    bool shared = false;
+    bool many = false;       // k_attend_many
     uint32_t step = 0;       // tokens per step
     uint32_t area_bytes = 0; // LDS besides the tables
     uint32_t row_tiles = 1, splits = 1;
@@ -717,16 +900,14 @@ hipError_t launch_attention_bf16(const AttnArgs& a, const AttnPlan& p, uint32_t 
 hipError_t launch_attention_fp16(const AttnArgs& a, const AttnPlan& p, uint32_t head_dim, uint32_t page_tokens,
                                  bool tree, uint32_t lds, hipStream_t s);
 
-template <class E, int D, int T, int MR, bool SHARED, bool TREE>
-static hipError_t launch_attend(const AttnArgs& a, uint32_t lds, hipStream_t s) {
+template <class K>
+static hipError_t launch_attend(K kernel, const AttnArgs& a, uint32_t waves, uint32_t lds, hipStream_t s) {
     if (lds > kMaxLdsPerBlock) {  // more than 64 KiB has to be asked for
-        const hipError_t e =
-            hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend<E, D, T, MR, SHARED, TREE>),
-                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((k_attend<E, D, T, MR, SHARED, TREE>), dim3(a.splits * a.work * a.row_tiles),
-                       dim3(kWave * kAttnWaves), lds, s, a);
+    hipLaunchKernelGGL(kernel, dim3(a.splits * a.work * a.row_tiles), dim3(kWave * waves), lds, s, a);
     return hipGetLastError();
 }
 
@@ -735,14 +916,14 @@ static hipError_t launch_attention_t(const AttnArgs& a, const AttnPlan& p, bool 
     hipError_t e;
     constexpr int M2 = D <= 128 ? 2 : 1;  // 32 rows of 256 dims would not leave registers for two waves per SIMD
     if (!tree)
-        e = p.mr == 1 ? launch_attend<E, D, T, 1, false, false>(a, lds, s)
-                      : launch_attend<E, D, T, M2, false, false>(a, lds, s);
-    else if (!p.shared)
-        e = p.mr == 1 ? launch_attend<E, D, T, 1, false, true>(a, lds, s)
-                      : launch_attend<E, D, T, M2, false, true>(a, lds, s);
+        e = p.mr == 1 ? launch_attend(k_attend_few<E, D, T, 1, false>, a, kFewWaves, lds, s)
+                      : launch_attend(k_attend_few<E, D, T, M2, false>, a, kFewWaves, lds, s);
+    else if (!p.many)
+        e = p.mr == 1 ? launch_attend(k_attend_few<E, D, T, 1, true>, a, kFewWaves, lds, s)
+                      : launch_attend(k_attend_few<E, D, T, M2, true>, a, kFewWaves, lds, s);
     else
-        e = p.mr == 1 ? launch_attend<E, D, T, 1, true, true>(a, lds, s)
-                      : launch_attend<E, D, T, M2, true, true>(a, lds, s);
+        e = p.mr == 1 ? launch_attend(k_attend_many<E, D, T, 1>, a, kManyWaves, lds, s)
+                      : launch_attend(k_attend_many<E, D, T, M2>, a, kManyWaves, lds, s);
     if (e != hipSuccess || a.splits == 1) return e;
     const uint64_t threads = a.n_rows * a.kv_heads * a.group * (D / 4);
     hipLaunchKernelGGL((k_join<E, D>), dim3((uint32_t)((threads + 255) / 256)), dim3(256), 0, s, a);

@@ -117,64 +117,102 @@ __device__ __forceinline__ void stage_page(const u32x4* st, uint32_t* stage) {
 //
 // The rebuild is the codec's: a lane's four words take p ? 32 - k : 32 bits
 // each, a wave scan gives their start bits, a funnel shift cuts the field out
-// of two words of the record, and the field's runs go to their places.  The
-// loop over s is not unrolled: unrolled, its table and record reads were
-// hoisted together and the attention kernels spilled registers.  With a
-// period of at most 256 words (one step) a lane's positions are the same in
-// every step, and its table entries are read once.
-template <int NV, class Sink>
-__device__ __forceinline__ bool rebuild_page(const Pool& p, const PageTab& tab, const uint32_t* stage, Sink sink) {
-    const uint32_t lane = lane_id();
-    __builtin_amdgcn_wave_barrier();
+// of two words of the record, and the field's runs go to their places.  It is
+// a chain of latencies (header, scan, record, tables), so U steps of 256 words
+// go through it together where the table entries allow: with a period of at
+// most 256 words a lane's positions are the same in every step and its
+// entries are read once.  (Attention over eight streams, 61 % of the value
+// pages records, 16-token pages of 128 dims: 4,500 cycles a page one step at
+// a time.)  With longer periods a step's entries fill the registers.
+template <int U, class Sink>
+__device__ __forceinline__ void rebuild_steps(const Pool& p, const PageTab& tab, const uint32_t* stage, uint32_t s0,
+                                              bool read, u32x4& kd, u32x4& bv, u32x4 (&rm)[3], uint32_t& carry,
+                                              Sink sink) {
+    const uint32_t lane = lane_id(), lg = p.log2g, runs = tab.runs, dxr = page_dx_rows(runs);
     const uint32_t* pay = stage + p.hw;
-    const uint32_t lg = p.log2g, runs = tab.runs, dxr = page_dx_rows(runs);
-    const bool ok = p.valid >= 32 || (stage[p.hw - 1] >> p.valid) == 0;
-    uint32_t carry = 0;
-    u32x4 kd = {0u, 0u, 0u, 0u}, bv = kd, rm[3] = {kd, kd, kd};
-#pragma unroll 1
-    for (int s = 0; s < NV; ++s) {
-        const uint32_t w0 = 256u * s + 4u * lane;
-        const uint32_t pos = w0 & (tab.stride - 1);
-        if (s == 0 || tab.stride > 256u) {
-            kd = tab_vector(tab, 0, 0, pos);
-            bv = tab_vector(tab, 1, -1, pos);
+    const uint32_t pos = (256u * s0 + 4u * lane) & (tab.stride - 1);
+    uint32_t h[U], off[U];
 #pragma unroll
-            for (uint32_t r = 0; r < 3; ++r)
-                if (r < runs) rm[r] = tab_vector(tab, 2 + dxr + r, 5 + r, pos);
-        }
-        const uint32_t c0 = w0 >> lg;
-        const uint32_t h = stage[c0 >> 5] >> (c0 & 31u);
-        uint32_t part[4], size[4], tot = 0;
+    for (int u = 0; u < U; ++u) {
+        const uint32_t c0 = (256u * (s0 + u) + 4u * lane) >> lg;
+        h[u] = stage[c0 >> 5] >> (c0 & 31u);
+    }
+    if (read) {
+        kd = tab_vector(tab, 0, 0, pos);
+        bv = tab_vector(tab, 1, -1, pos);
+#pragma unroll
+        for (uint32_t r = 0; r < 3; ++r)
+            if (r < runs) rm[r] = tab_vector(tab, 2 + dxr + r, 5 + r, pos);
+    }
+    auto part = [&](int u, int j) __attribute__((always_inline)) { return (h[u] >> ((uint32_t)j >> lg)) & 1u; };
+    uint32_t tot[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        tot[u] = 128u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tot[u] -= part(u, j) ? kd[j] & 63u : 0u;
+        off[u] = tot[u];
+    }
+    // U wave scans side by side (wave_incl_scan)
+#define IBP_SCAN_STEP(ctrl, rows)                                                                        \
+    _Pragma("unroll") for (int u = 0; u < U; ++u)                                                        \
+        off[u] += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)off[u], ctrl, rows, 0xf, false);
+    IBP_SCAN_STEP(0x111, 0xf)
+    IBP_SCAN_STEP(0x112, 0xf)
+    IBP_SCAN_STEP(0x114, 0xf)
+    IBP_SCAN_STEP(0x118, 0xf)
+    IBP_SCAN_STEP(0x142, 0xa)
+    IBP_SCAN_STEP(0x143, 0xc)
+#undef IBP_SCAN_STEP
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t end = lane_value(off[u], kWave - 1);
+        off[u] += carry - tot[u];
+        carry += end;
+    }
+    u32x4 f[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            part[j] = (h >> ((uint32_t)j >> lg)) & 1u;
-            size[j] = part[j] ? 32u - (kd[j] & 63u) : 32u;
-            tot += size[j];
+            const uint32_t q = off[u] >> 5;
+            f[u][j] = funnel(pay[q + 1], pay[q], off[u]);
+            off[u] += 32u - (part(u, j) ? kd[j] & 63u : 0u);
         }
-        const uint32_t incl = wave_incl_scan(tot);
-        uint32_t off = carry + incl - tot;
-        carry += lane_value(incl, kWave - 1);
-        uint32_t f[4];
+    }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t q = off >> 5;
-            f[j] = funnel(pay[q + 1], pay[q], off);
-            off += size[j];
-        }
+    for (int u = 0; u < U; ++u) {
         u32x4 x = bv;
 #pragma unroll
         for (uint32_t r = 0; r < 3; ++r)  // (rows that are not there stay zero)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] |= (f[j] << ((kd[j] >> (8 * (r + 1))) & 31u)) & rm[r][j];
-        for (uint32_t r = 3; r < runs; ++r) {
+            for (int j = 0; j < 4; ++j) x[j] |= (f[u][j] << ((kd[j] >> (8 * (r + 1))) & 31u)) & rm[r][j];
+        for (uint32_t r = 3; U == 1 && r < runs; ++r) {
             const u32x4 m = tab_vector(tab, 2 + dxr + r, 5 + r, pos);
             const u32x4 dv = tab_vector(tab, 2 + ((r - 3) >> 2), 1 + ((r - 3) >> 2), pos);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] |= (f[j] << ((dv[j] >> (8 * ((r - 3) & 3u))) & 31u)) & m[j];
+            for (int j = 0; j < 4; ++j) x[j] |= (f[u][j] << ((dv[j] >> (8 * ((r - 3) & 3u))) & 31u)) & m[j];
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = part[j] ? x[j] : f[j];
-        sink(w0, x);
+        for (int j = 0; j < 4; ++j) x[j] = part(u, j) ? x[j] : f[u][j];
+        sink(256u * (s0 + u) + 4u * lane, x);
+    }
+}
+
+template <int NV, int U, class Sink>
+__device__ __forceinline__ bool rebuild_page(const Pool& p, const PageTab& tab, const uint32_t* stage, Sink sink) {
+    static_assert(NV % U == 0, "whole groups of steps");
+    __builtin_amdgcn_wave_barrier();
+    const bool ok = p.valid >= 32 || (stage[p.hw - 1] >> p.valid) == 0;
+    uint32_t carry = 0;
+    u32x4 kd = {0u, 0u, 0u, 0u}, bv = kd, rm[3] = {kd, kd, kd};
+    if (U > 1 && tab.stride <= 256u && tab.runs <= 3) {
+#pragma unroll 1
+        for (int s = 0; s < NV; s += U) rebuild_steps<U>(p, tab, stage, s, s == 0, kd, bv, rm, carry, sink);
+    } else {
+#pragma unroll 1
+        for (int s = 0; s < NV; ++s)
+            rebuild_steps<1>(p, tab, stage, s, s == 0 || tab.stride > 256u, kd, bv, rm, carry, sink);
     }
     __builtin_amdgcn_wave_barrier();
     return ok && p.hw + (carry + 31) / 32 < 256u * NV;

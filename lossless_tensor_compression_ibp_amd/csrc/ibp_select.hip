@@ -81,7 +81,7 @@ __global__ __launch_bounds__(kWave * kBoundWaves) void k_page_bounds(Pool pool, 
         };
         if (uniform(page_bit(pool.bitmask, id))) {
             stage_page<NV>(st, stage);
-            if (!rebuild_page<NV>(pool, tab, stage, take)) latch_error(pool.err, kErrCorrupt);
+            if (!rebuild_page<NV, 2>(pool, tab, stage, take)) latch_error(pool.err, kErrCorrupt);
         } else {
 #pragma unroll
             for (int r = 0; r < NV; ++r) take(256u * r + 4u * lane, st[r]);
