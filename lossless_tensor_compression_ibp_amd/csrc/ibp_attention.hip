@@ -16,7 +16,6 @@ namespace {
 // Waves that a launch should have: eight per compute unit of an MI355X.
 constexpr uint64_t kTargetWaves = 2048;
 constexpr uint64_t kMaxSplits = 256;
-constexpr uint64_t kLdsLimit = 160 * 1024 - 2048;  // the kernels' static arrays aside
 
 // Rows per workgroup, split of the context, LDS.  `rows`: most rows of one
 // (sequence or row, key/value head).

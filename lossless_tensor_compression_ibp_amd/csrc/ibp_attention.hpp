@@ -33,6 +33,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ibp_kv_math.hpp"
 
 namespace ibp {
@@ -304,14 +306,13 @@ struct Rows {
     __device__ __forceinline__ void scores(const char* keys, int stride) {
         const uint32_t col = lane_id() & 15u, g = lane_id() >> 4;
 #pragma unroll
-        for (int u = 0; u < TILES; ++u) {
+        for (int kk = 0; kk < DK; ++kk) {
 #pragma unroll
-            for (int t = 0; t < MR; ++t) s[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int kk = 0; kk < DK; ++kk) {
+            for (int u = 0; u < TILES; ++u) {
                 const V8 kf = *reinterpret_cast<const V8*>(keys + (16 * u + col) * stride + 64 * kk + 16 * g);
 #pragma unroll
-                for (int t = 0; t < MR; ++t) s[t][u] = E::mfma(kf, q[t][kk], s[t][u]);
+                for (int t = 0; t < MR; ++t)
+                    s[t][u] = E::mfma(kf, q[t][kk], kk ? s[t][u] : f32x4{0.f, 0.f, 0.f, 0.f});
             }
         }
     }
@@ -323,47 +324,56 @@ struct Rows {
         for (int e = 0; e < 4; ++e) s[t][u][e] = (seen >> (4 * g + e)) & 1u ? s[t][u][e] : -__builtin_inff();
     }
 
-    // The running maximum and the weights, which take the scores' place.
-    __device__ __forceinline__ void weights(float scale2) {
+    // The running maximum.  It is moved only when a score passes it by more
+    // than 8 (weights then stay below 2^8 and sums far from overflow), so most
+    // steps rescale nothing; one branch for all rows leaves the rest of a step
+    // in one block, where the compiler can run weights beside products.
+    __device__ __forceinline__ void raise(float scale2) {
+        float top[MR];
+        bool move = false;
 #pragma unroll
         for (int t = 0; t < MR; ++t) {
-            float top = -__builtin_inff();
+            float x[TILES];
 #pragma unroll
-            for (int u = 0; u < TILES; ++u) {
+            for (int u = 0; u < TILES; ++u)
+                x[u] = fmaxf(fmaxf(s[t][u][0], s[t][u][1]), fmaxf(s[t][u][2], s[t][u][3]));
+            top[t] = x[0];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) top = fmaxf(top, s[t][u][e]);
-            }
-            top = max_over_four(top) * scale2;
-            // The maximum is moved only when a score passes it by more than
-            // 8 (weights then stay below 2^8 and sums far from overflow), so
-            // most steps rescale nothing.
-            if (ballot(top > m[t] + 8.f || (m[t] == -__builtin_inff() && top != -__builtin_inff()))) {
-                const float m_new = fmaxf(m[t], top);
+            for (int u = 1; u < TILES; ++u) top[t] = fmaxf(top[t], x[u]);
+            top[t] = max_over_four(top[t]) * scale2;
+            move = move || top[t] > m[t] + 8.f || (m[t] == -__builtin_inff() && top[t] != -__builtin_inff());
+        }
+        if (ballot(move)) {
+#pragma unroll
+            for (int t = 0; t < MR; ++t) {
+                const float m_new = fmaxf(m[t], top[t]);
                 const float f = m_new == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(m[t] - m_new);
                 m[t] = m_new;
                 l[t] *= f;
 #pragma unroll
                 for (int n = 0; n < DN; ++n) o[t][n] *= f;
             }
-            const float base = m[t] == -__builtin_inff() ? 0.f : -m[t];
-#pragma unroll
-            for (int u = 0; u < TILES; ++u) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[t][u][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][u][e], scale2, base));
-                l[t] += (s[t][u][0] + s[t][u][1]) + (s[t][u][2] + s[t][u][3]);
-            }
         }
     }
 
-    // O^T += V^T P^T
-    __device__ __forceinline__ void values(const char* vals, int stride) {
+    // Weights, their sum, and O^T += V^T P^T, two tiles of tokens at a time.
+    __device__ __forceinline__ void values(const char* vals, int stride, float scale2) {
         const uint32_t col = lane_id() & 15u, g = lane_id() >> 4;
+        float base[MR];
+#pragma unroll
+        for (int t = 0; t < MR; ++t) base[t] = m[t] == -__builtin_inff() ? 0.f : -m[t];
 #pragma unroll
         for (int u = 0; u < TILES; u += 2) {
             V8 p[MR];
 #pragma unroll
             for (int t = 0; t < MR; ++t) {
+#pragma unroll
+                for (int v = u; v < u + 2; ++v) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[t][v][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][v][e], scale2, base[t]));
+                    l[t] += (s[t][v][0] + s[t][v][1]) + (s[t][v][2] + s[t][v][3]);
+                }
                 const u32x4 x = {E::pack(s[t][u][0], s[t][u][1]), E::pack(s[t][u][2], s[t][u][3]),
                                  E::pack(s[t][u + 1][0], s[t][u + 1][1]), E::pack(s[t][u + 1][2], s[t][u + 1][3])};
                 p[t] = bits_as<V8>(x);
@@ -640,7 +650,7 @@ __global__ __launch_bounds__(kWave * kFewWaves, 2) void k_attend_few(AttnArgs a)
                 }
             }
         }
-        rows.weights(a.scale2);
+        rows.raise(a.scale2);
         u32x4* const st_v = S::ONE ? st_a : st_b;
         if (draft) {
 #pragma unroll
@@ -654,7 +664,7 @@ __global__ __launch_bounds__(kWave * kFewWaves, 2) void k_attend_few(AttnArgs a)
                 load(st_b, i + 1, true, id_v);
             advance(i + 1);
         }
-        rows.values(tile, S::RV);
+        rows.values(tile, S::RV, a.scale2);
         lds_order();
         if (more) take_sees();
     }
@@ -832,8 +842,8 @@ __global__ __launch_bounds__(kWave * kManyWaves, 2) void k_attend_many(AttnArgs 
                 }
             }
         }
-        rows.weights(a.scale2);
-        rows.values(area + STEP * S::RK, S::RV);
+        rows.raise(a.scale2);
+        rows.values(area + STEP * S::RK, S::RV, a.scale2);
     }
 
     const ArgsPtr c = args_again();
@@ -869,17 +879,38 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a) {
     }
     if (rh >= rows * nq) return;
     if (a.new_rows && a.new_rows[0] > 0 && rh < (uint64_t)a.new_rows[0] * nq) return;
+    // Lane j of the row's takes the maximum and sum of split j (and j + D / 4,
+    // ...), so that they arrive in one latency; then four splits' numbers at a
+    // time.
+    constexpr int W = D / 4;
     const float* ml = a.part_ml + rh * a.splits * 2;
     const float* part = a.part + rh * a.splits * D + d;
+    const uint32_t lane = (uint32_t)(e % W);
     float mm = -__builtin_inff(), ll = 0.f;
-    for (uint32_t s = 0; s < a.splits; ++s) mm = fmaxf(mm, ml[2 * s]);
+    for (uint32_t s = lane; s < a.splits; s += W) mm = fmaxf(mm, ml[2 * s]);
+    for (int o = W / 2; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o));
     const float base = mm == -__builtin_inff() ? 0.f : mm;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    for (uint32_t s = 0; s < a.splits; ++s) {
-        const float f = __builtin_amdgcn_exp2f(ml[2 * s] - base);
-        ll += f * ml[2 * s + 1];
-        x += f * *reinterpret_cast<const f32x4*>(part + (uint64_t)s * D);
+    for (uint32_t s0 = 0; s0 < a.splits; s0 += W) {
+        float f = 0.f;
+        if (s0 + lane < a.splits) {
+            f = __builtin_amdgcn_exp2f(ml[2 * (s0 + lane)] - base);
+            ll += f * ml[2 * (s0 + lane) + 1];
+        }
+        const uint32_t n = min(a.splits - s0, (uint32_t)W);
+        for (uint32_t s = 0; s < n; s += 4) {
+            f32x4 y[4];
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u)
+                y[u] = *reinterpret_cast<const f32x4*>(part + (uint64_t)(s0 + min(s + u, n - 1)) * D);
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u) {
+                const float g = __shfl(f, (int)(threadIdx.x - lane + s + u) & 63);
+                if (s + u < n) x += g * y[u];
+            }
+        }
     }
+    for (int o = W / 2; o > 0; o >>= 1) ll += __shfl_xor(ll, o);
     const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
     const u32x2 y = {E::pack(x[0] * inv, x[1] * inv), E::pack(x[2] * inv, x[3] * inv)};
     *reinterpret_cast<u32x2*>(a.out + rh * D + d) = y;
@@ -900,11 +931,22 @@ hipError_t launch_attention_bf16(const AttnArgs& a, const AttnPlan& p, uint32_t 
 hipError_t launch_attention_fp16(const AttnArgs& a, const AttnPlan& p, uint32_t head_dim, uint32_t page_tokens,
                                  bool tree, uint32_t lds, hipStream_t s);
 
-template <class K>
-static hipError_t launch_attend(K kernel, const AttnArgs& a, uint32_t waves, uint32_t lds, hipStream_t s) {
-    if (lds > kMaxLdsPerBlock) {  // more than 64 KiB has to be asked for
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+constexpr uint64_t kLdsLimit = kLdsPerCu - 2048;  // of dynamic LDS: the kernels' static arrays aside
+
+// More than 64 KiB of LDS has to be asked for, once per kernel and device (the
+// call costs about as much as a launch).
+template <auto kernel>
+static hipError_t launch_attend(const AttnArgs& a, uint32_t waves, uint32_t lds, hipStream_t s) {
+    static std::atomic<uint64_t> asked{0};
+    if (lds > kMaxLdsPerBlock) {
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        const uint64_t bit = 1ull << (dev & 63);
+        if (e == hipSuccess && !(asked.load(std::memory_order_relaxed) & bit)) {
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)kLdsLimit);
+            if (e == hipSuccess && dev < 64) asked.fetch_or(bit, std::memory_order_relaxed);
+        }
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL(kernel, dim3(a.splits * a.work * a.row_tiles), dim3(kWave * waves), lds, s, a);
@@ -916,14 +958,14 @@ static hipError_t launch_attention_t(const AttnArgs& a, const AttnPlan& p, bool 
     hipError_t e;
     constexpr int M2 = D <= 128 ? 2 : 1;  // 32 rows of 256 dims would not leave registers for two waves per SIMD
     if (!tree)
-        e = p.mr == 1 ? launch_attend(k_attend_few<E, D, T, 1, false>, a, kFewWaves, lds, s)
-                      : launch_attend(k_attend_few<E, D, T, M2, false>, a, kFewWaves, lds, s);
+        e = p.mr == 1 ? launch_attend<k_attend_few<E, D, T, 1, false>>(a, kFewWaves, lds, s)
+                      : launch_attend<k_attend_few<E, D, T, M2, false>>(a, kFewWaves, lds, s);
     else if (!p.many)
-        e = p.mr == 1 ? launch_attend(k_attend_few<E, D, T, 1, true>, a, kFewWaves, lds, s)
-                      : launch_attend(k_attend_few<E, D, T, M2, true>, a, kFewWaves, lds, s);
+        e = p.mr == 1 ? launch_attend<k_attend_few<E, D, T, 1, true>>(a, kFewWaves, lds, s)
+                      : launch_attend<k_attend_few<E, D, T, M2, true>>(a, kFewWaves, lds, s);
     else
-        e = p.mr == 1 ? launch_attend(k_attend_many<E, D, T, 1>, a, kManyWaves, lds, s)
-                      : launch_attend(k_attend_many<E, D, T, M2>, a, kManyWaves, lds, s);
+        e = p.mr == 1 ? launch_attend<k_attend_many<E, D, T, 1>>(a, kManyWaves, lds, s)
+                      : launch_attend<k_attend_many<E, D, T, M2>>(a, kManyWaves, lds, s);
     if (e != hipSuccess || a.splits == 1) return e;
     const uint64_t threads = a.n_rows * a.kv_heads * a.group * (D / 4);
     hipLaunchKernelGGL((k_join<E, D>), dim3((uint32_t)((threads + 255) / 256)), dim3(256), 0, s, a);

@@ -28,7 +28,7 @@ namespace ibp {
 
 constexpr uint32_t kPageWaves = 4;        // waves (items) per workgroup of the copies
 constexpr uint32_t kCountBlock = 256;     // threads of the counting kernels
-constexpr uint32_t kCountPer = 16;        // slots per thread
+constexpr uint32_t kCountPer = 4;         // slots per thread
 constexpr uint32_t kCountSlots = kCountBlock * kCountPer;
 
 // Removed bits of the item's header, summed over the wave.  st[0] of lane l

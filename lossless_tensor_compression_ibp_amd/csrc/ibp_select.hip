@@ -32,9 +32,9 @@ namespace ibp {
 constexpr uint32_t kBoundWaves = 4;
 
 __device__ __forceinline__ void join_bounds(float& lo, float& hi, float x_lo, float x_hi) {
-    // comparisons with NaN are false: a NaN on either side is kept
-    lo = (x_lo < lo || x_lo != x_lo) ? x_lo : lo;
-    hi = (x_hi > hi || x_hi != x_hi) ? x_hi : hi;
+    // (minimum and maximum that pass a NaN on)
+    lo = __builtin_elementwise_minimum(lo, x_lo);
+    hi = __builtin_elementwise_maximum(hi, x_hi);
 }
 
 template <class E, int NV, bool TAB_LDS>
@@ -52,6 +52,7 @@ __global__ __launch_bounds__(kWave * kBoundWaves) void k_page_bounds(Pool pool, 
     const PageTab tab = page_tab(pool, smem, TAB_LDS);
     uint32_t* stage = smem + tab_words + wib * page_stage_words<NV>();
     const uint32_t row_lanes = row_words / 4;  // lanes that one token takes
+    const uint32_t row_shift = 31 - __builtin_clz(row_words);
     const uint64_t stride = (uint64_t)gridDim.x * kBoundWaves;
     for (uint64_t i = (uint64_t)blockIdx.x * kBoundWaves + wib; i < n; i += stride) {
         const int64_t id64 = (int64_t)uniform64((uint64_t)ids[i]);
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(kWave * kBoundWaves) void k_page_bounds(Pool pool, 
             hi[j] = -__builtin_inff();
         }
         auto take = [&](uint32_t w, const u32x4& x) __attribute__((always_inline)) {
-            if ((int32_t)(w / row_words) >= held) return;
+            if ((int32_t)(w >> row_shift) >= held) return;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float y = E::from_bits(x[j >> 1] >> (16 * (j & 1)));
@@ -145,10 +146,10 @@ struct SelectArgs {
 constexpr uint32_t kScoreWaves = 4;
 constexpr uint32_t kWaveBlocks = 64;
 
-// Error of a 32-bit sum of 2 * head_dim products, relative to the sum of
-// their absolute values: head_dim <= 256, so at most 512 additions of 2^-24
-// each, 2^-15; the products themselves are exact.
-constexpr float kSumError = 1.0f / 32768.0f;
+// Error of a 32-bit sum of 2 * dim products, relative to the sum of their
+// absolute values: 2 * dim additions, each off by at most 2^-23 (which covers
+// rounding towards zero inside the matrix cores); the products are exact.
+__host__ __device__ constexpr float sum_error(int dim) { return (float)dim / 4194304.0f; }
 
 // Blocks of row r (0 where its sequence or length is not valid).
 __device__ __forceinline__ uint32_t row_blocks(const SelectArgs& a, uint64_t r, int64_t* seq) {
@@ -558,7 +559,7 @@ __global__ __launch_bounds__(1024) void k_choose(SelectArgs a) {
         if (tid == 0) sh.n_near = 0;
         uint32_t slack_bits = __float_as_uint(slack), zero = 0;
         choose_max2(slack_bits, zero, sh, turn);  // (and the keys are in LDS)
-        slack = kSumError * __uint_as_float(slack_bits);
+        slack = sum_error(D) * __uint_as_float(slack_bits);
         const uint32_t own_at = max(at, f_end), own_end = min(end, l_begin);
         auto own = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll 1
