@@ -160,15 +160,13 @@ __device__ __forceinline__ uint32_t row_blocks(const SelectArgs& a, uint64_t r, 
     return (uint32_t)(nb < a.blocks ? nb : a.blocks);
 }
 
+// One wave: rows r0 .. of head h, blocks b_first .. of a.span * 64.
 template <class E, int D, int CT>
-__global__ __launch_bounds__(kWave * kScoreWaves, 2) void k_scores(SelectArgs a) {
+__device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, uint32_t h, uint32_t b_first) {
     using V8 = typename E::V8;
     constexpr int DK = D / 32;
-    const uint32_t lane = lane_id(), wib = uniform(threadIdx.x / kWave);
+    const uint32_t lane = lane_id();
     const uint32_t col = lane & 15u, g = lane >> 4;
-    const uint32_t h = blockIdx.y;
-    const uint64_t r0 = ((uint64_t)blockIdx.z * (a.same_blocks ? kScoreWaves : 1u) + (a.same_blocks ? wib : 0u)) * a.wave_rows;
-    const uint32_t b_first = (a.same_blocks ? blockIdx.x : blockIdx.x * kScoreWaves + wib) * kWaveBlocks * a.span;
     // lane l: row r0 + l of the wave (at most 64), its sequence and blocks
     int64_t my_seq = -1;
     uint32_t my_nb = 0;
@@ -336,6 +334,17 @@ __global__ __launch_bounds__(kWave * kScoreWaves, 2) void k_scores(SelectArgs a)
     }
 }
 
+template <class E, int D, int CT>
+__global__ __launch_bounds__(kWave * kScoreWaves, 2) void k_scores(SelectArgs a) {
+    const uint32_t wib = uniform(threadIdx.x / kWave);
+    if (a.same_blocks)
+        score_blocks<E, D, CT>(a, ((uint64_t)blockIdx.z * kScoreWaves + wib) * a.wave_rows, blockIdx.y,
+                               blockIdx.x * kWaveBlocks * a.span);
+    else
+        score_blocks<E, D, CT>(a, (uint64_t)blockIdx.z * a.wave_rows, blockIdx.y,
+                               (blockIdx.x * kScoreWaves + wib) * kWaveBlocks * a.span);
+}
+
 // ---------------------------------------------------------------------------
 // The choice.  One workgroup per (row, head).  A thread has consecutive
 // blocks, whose keys (scores as ordered integers) lie in LDS, or for rows too
@@ -500,9 +509,7 @@ __device__ __forceinline__ uint32_t exact_key(const SelectArgs& a, uint64_t r, u
 }
 
 template <class E, int D, bool KEYS>
-__global__ __launch_bounds__(1024) void k_choose(SelectArgs a) {
-    __shared__ ChooseShared sh;
-    extern __shared__ __align__(16) uint32_t smem[];
+__device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared& sh, uint32_t* smem) {
     uint32_t* const near_words = smem;  // blocks to be summed in 64 bits
     uint32_t* const keys = smem + (a.blocks + 31) / 32;
     const uint64_t rh = blockIdx.x;
@@ -704,6 +711,34 @@ __global__ __launch_bounds__(1024) void k_choose(SelectArgs a) {
     for (uint32_t i = total + tid; i < a.n_out; i += nt) out[i] = -1;
 }
 
+template <class E, int D, bool KEYS>
+__global__ __launch_bounds__(1024) void k_choose(SelectArgs a) {
+    __shared__ ChooseShared sh;
+    extern __shared__ __align__(16) uint32_t smem[];
+    choose_blocks<E, D, KEYS>(a, sh, smem);
+}
+
+// Both in one launch, for rows with pages of their own in tables of at most
+// kOneLaunchBlocks blocks: the workgroup of a (row, head) scores its blocks,
+// 64 a wave at a time, and chooses among them.  (A row of 256 blocks and 8
+// heads of 128 dims: 8 and 6 us in two launches.)
+constexpr uint32_t kSelectWaves = 8;
+constexpr uint64_t kOneLaunchBlocks = 1024;
+
+template <class E, int D>
+__global__ __launch_bounds__(kWave * kSelectWaves) void k_select(SelectArgs a) {
+    __shared__ ChooseShared sh;
+    extern __shared__ __align__(16) uint32_t smem[];
+    const uint64_t r = blockIdx.x / a.kv_heads;
+    const uint32_t h = blockIdx.x % a.kv_heads;
+#pragma unroll 1
+    for (uint32_t b = uniform(threadIdx.x / kWave) * kWaveBlocks; b < a.blocks; b += kSelectWaves * kWaveBlocks)
+        score_blocks<E, D, 1>(a, r, h, b);
+    __threadfence_block();
+    __syncthreads();
+    choose_blocks<E, D, true>(a, sh, smem);
+}
+
 }  // namespace ibp
 
 using namespace ibp;
@@ -833,18 +868,23 @@ ibp_status ibp_select_pages(ibp_meta_t h, const ibp_attention* a, const void* q,
     auto launch = [&](auto e, auto dc) {
         using E = decltype(e);
         constexpr int D = decltype(dc)::value;
+        const dim3 grid((uint32_t)(a->n_rows * a->n_kv_heads));
+        const uint32_t marks = (uint32_t)(4 * ((a->table_blocks + 31) / 32));
+        if (scored && !shared && a->table_blocks <= kOneLaunchBlocks) {
+            hipLaunchKernelGGL((k_select<E, D>), grid, dim3(kWave * kSelectWaves),
+                               marks + (uint32_t)(4 * a->table_blocks), stream, s);
+            return hipGetLastError();
+        }
         if (scored) {  // no row can have more pages than it may read otherwise
             const uint64_t per_wg = (uint64_t)(shared ? 1 : kScoreWaves) * kWaveBlocks * s.span;
-            const dim3 grid((uint32_t)((a->table_blocks + per_wg - 1) / per_wg), a->n_kv_heads, (uint32_t)groups);
+            const dim3 tiles((uint32_t)((a->table_blocks + per_wg - 1) / per_wg), a->n_kv_heads, (uint32_t)groups);
             if (shared)
-                hipLaunchKernelGGL((k_scores<E, D, D == 256 ? 1 : 2>), grid, dim3(kWave * kScoreWaves), 0, stream, s);
+                hipLaunchKernelGGL((k_scores<E, D, D == 256 ? 1 : 2>), tiles, dim3(kWave * kScoreWaves), 0, stream, s);
             else
-                hipLaunchKernelGGL((k_scores<E, D, 1>), grid, dim3(kWave * kScoreWaves), 0, stream, s);
+                hipLaunchKernelGGL((k_scores<E, D, 1>), tiles, dim3(kWave * kScoreWaves), 0, stream, s);
             const hipError_t err = hipGetLastError();
             if (err != hipSuccess) return err;
         }
-        const dim3 grid((uint32_t)(a->n_rows * a->n_kv_heads));
-        const uint32_t marks = (uint32_t)(4 * ((a->table_blocks + 31) / 32));
         if (a->table_blocks <= kLdsKeys) {
             // eight blocks per thread
             const uint32_t waves =
