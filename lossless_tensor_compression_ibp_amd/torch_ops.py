@@ -12,6 +12,9 @@ returns an integer key that the ops take instead.  Each op also has a fake
     key = torch_ops.register(ibp.ibp_build_metadata(sample, 1024, L, W, M, T))
     slots, bitmask, stored = torch.ops.ibp.compress(key, rows)
     batch = torch.ops.ibp.gather_decompress(key, slots, bitmask, ids)
+
+A cache of pages is passed as the handle's key, the slots (n, L) and the
+bitmask; the attention ops take one of keys and one of values.
 """
 from __future__ import annotations
 
@@ -112,6 +115,104 @@ def gather_decompress(key: int, slots: torch.Tensor, bitmask: torch.Tensor, ids:
 @gather_decompress.register_fake
 def _(key: int, slots: torch.Tensor, bitmask: torch.Tensor, ids: torch.Tensor):
     return torch.empty((ids.numel(), slots.shape[1]), dtype=torch.uint8, device=ids.device)
+
+
+def _pages(key: int, slots: torch.Tensor, bitmask: torch.Tensor) -> ibp.Pages:
+    return ibp.Pages(_meta(key), slots, slots.shape[0], bitmask)
+
+
+@torch.library.custom_op("ibp::pages_copy", mutates_args=("dst_slots", "dst_bitmask"))
+def pages_copy(key: int, src_slots: torch.Tensor, src_bitmask: torch.Tensor, src_ids: torch.Tensor,
+               dst_slots: torch.Tensor, dst_bitmask: torch.Tensor, dst_ids: torch.Tensor) -> None:
+    """Items and bits of slots src_ids -> slots dst_ids, without decoding."""
+    ibp.ibp_pages_copy(_meta(key), src_slots, src_slots.shape[0], src_bitmask, src_ids, dst_slots, dst_slots.shape[0],
+                       dst_bitmask, dst_ids)
+
+
+@pages_copy.register_fake
+def _(key: int, src_slots: torch.Tensor, src_bitmask: torch.Tensor, src_ids: torch.Tensor, dst_slots: torch.Tensor,
+      dst_bitmask: torch.Tensor, dst_ids: torch.Tensor):
+    return None
+
+
+@torch.library.custom_op("ibp::page_bounds", mutates_args=("bounds",))
+def page_bounds(key: int, slots: torch.Tensor, bitmask: torch.Tensor, ids: torch.Tensor, tokens: torch.Tensor | None,
+                bounds: torch.Tensor) -> None:
+    """bounds[id] (2, dims) <- smallest and largest number of the first tokens
+    of pages ids (tokens None: of whole pages)."""
+    ibp.ibp_page_bounds(_pages(key, slots, bitmask), ids, tokens, bounds)
+
+
+@page_bounds.register_fake
+def _(key: int, slots: torch.Tensor, bitmask: torch.Tensor, ids: torch.Tensor, tokens: torch.Tensor | None,
+      bounds: torch.Tensor):
+    return None
+
+
+@torch.library.custom_op("ibp::select_pages", mutates_args=())
+def select_pages(key: int, q: torch.Tensor, bounds: torch.Tensor, k_table: torch.Tensor, lens: torch.Tensor, n: int,
+                 page_tokens: int, keep_first: int = 0, keep_last: int = 0,
+                 row_seq: torch.Tensor | None = None) -> torch.Tensor:
+    """Block numbers (rows, key/value heads, n) that each query reads."""
+    blocks = torch.empty((q.shape[0], k_table.shape[1], n), dtype=torch.int32, device=q.device)
+    ibp.ibp_select_pages(q, bounds, k_table, lens, blocks, meta=_meta(key), page_tokens=page_tokens,
+                         keep_first=keep_first, keep_last=keep_last, row_seq=row_seq)
+    return blocks
+
+
+@select_pages.register_fake
+def _(key: int, q: torch.Tensor, bounds: torch.Tensor, k_table: torch.Tensor, lens: torch.Tensor, n: int,
+      page_tokens: int, keep_first: int = 0, keep_last: int = 0, row_seq: torch.Tensor | None = None):
+    return torch.empty((q.shape[0], k_table.shape[1], n), dtype=torch.int32, device=q.device)
+
+
+def _out_and_lse(q: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    return (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+            torch.empty(q.shape[:2], dtype=torch.float32, device=q.device))
+
+
+@torch.library.custom_op("ibp::sparse_attention", mutates_args=())
+def sparse_attention(k_key: int, k_slots: torch.Tensor, k_bitmask: torch.Tensor, v_key: int, v_slots: torch.Tensor,
+                     v_bitmask: torch.Tensor, q: torch.Tensor, k_table: torch.Tensor, v_table: torch.Tensor,
+                     lens: torch.Tensor, blocks: torch.Tensor, scale: float,
+                     row_seq: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(out, log-sum-exp) of each row over the pages that blocks lists for it."""
+    out, lse = _out_and_lse(q)
+    ibp.ibp_sparse_attention(_pages(k_key, k_slots, k_bitmask), _pages(v_key, v_slots, v_bitmask), q, k_table, v_table,
+                             lens, blocks, out, lse, scale=scale, row_seq=row_seq)
+    return out, lse
+
+
+@sparse_attention.register_fake
+def _(k_key: int, k_slots: torch.Tensor, k_bitmask: torch.Tensor, v_key: int, v_slots: torch.Tensor,
+      v_bitmask: torch.Tensor, q: torch.Tensor, k_table: torch.Tensor, v_table: torch.Tensor, lens: torch.Tensor,
+      blocks: torch.Tensor, scale: float, row_seq: torch.Tensor | None = None):
+    return _out_and_lse(q)
+
+
+@torch.library.custom_op("ibp::tree_attention", mutates_args=())
+def tree_attention(k_key: int, k_slots: torch.Tensor, k_bitmask: torch.Tensor, v_key: int, v_slots: torch.Tensor,
+                   v_bitmask: torch.Tensor, q: torch.Tensor, k_table: torch.Tensor, v_table: torch.Tensor,
+                   lens: torch.Tensor, new_rows: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                   mask: torch.Tensor, scale: float, max_new: int,
+                   max_len: int = 0) -> tuple[torch.Tensor, torch.Tensor]:
+    """(out, log-sum-exp) of drafted tokens over their sequence's pages and the
+    drafted tokens that mask has.  Rows that belong to no sequence are zero,
+    and their log-sum-exp minus infinity."""
+    out, lse = _out_and_lse(q)
+    out.zero_()
+    lse.fill_(float("-inf"))
+    ibp.ibp_tree_attention(_pages(k_key, k_slots, k_bitmask), _pages(v_key, v_slots, v_bitmask), q, k_table, v_table,
+                           lens, new_rows, k_new, v_new, mask, out, lse, scale=scale, max_len=max_len, max_new=max_new)
+    return out, lse
+
+
+@tree_attention.register_fake
+def _(k_key: int, k_slots: torch.Tensor, k_bitmask: torch.Tensor, v_key: int, v_slots: torch.Tensor,
+      v_bitmask: torch.Tensor, q: torch.Tensor, k_table: torch.Tensor, v_table: torch.Tensor, lens: torch.Tensor,
+      new_rows: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, mask: torch.Tensor, scale: float, max_new: int,
+      max_len: int = 0):
+    return _out_and_lse(q)
 
 
 def check(key: int) -> None:
