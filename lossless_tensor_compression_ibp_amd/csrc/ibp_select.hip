@@ -711,8 +711,12 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
     for (uint32_t i = total + tid; i < a.n_out; i += nt) out[i] = -1;
 }
 
+// 64 registers for pages of up to 128 dims, so that eight waves fit a SIMD: the
+// 64-bit sums read from everywhere and wait (2,048 rows of 512 blocks on 8
+// heads: 91 us, 124 us with the 94 registers the compiler takes by itself).
+// 256 dims would spill.
 template <class E, int D, bool KEYS>
-__global__ __launch_bounds__(1024) void k_choose(SelectArgs a) {
+__global__ __launch_bounds__(1024, D <= 128 ? 8 : 4) void k_choose(SelectArgs a) {
     __shared__ ChooseShared sh;
     extern __shared__ __align__(16) uint32_t smem[];
     choose_blocks<E, D, KEYS>(a, sh, smem);
