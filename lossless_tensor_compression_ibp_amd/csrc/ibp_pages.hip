@@ -30,6 +30,15 @@ constexpr uint32_t kPageWaves = 4;        // waves (items) per workgroup of the 
 constexpr uint32_t kCountBlock = 256;     // threads of the counting kernels
 constexpr uint32_t kCountPer = 4;         // slots per thread
 constexpr uint32_t kCountSlots = kCountBlock * kCountPer;
+// The free slots that a fork may take are counted and listed in one launch in
+// pools of up to kListSlots slots: its workgroups (of kListBlock threads) each
+// read all counts, at most 16 loads of 16 bytes per thread.  With 32,768 slots
+// that is 6.7 us on the GPU against 5.4 in two launches, but forks are bound by
+// the host, for which a launch is 4 to 5 us (fork and free 28.8 us, 34.3 with
+// the second launch).  The plan of a compaction, bound by the GPU, took 10.4 us
+// this way with 65,536 slots and 6.8 in two launches, which it keeps.
+constexpr uint32_t kListBlock = 1024;
+constexpr uint64_t kListSlots = 65536;
 
 // Removed bits of the item's header, summed over the wave.  st[0] of lane l
 // holds words 4 l .. 4 l + 3 of the slot, which include every header word
@@ -168,14 +177,32 @@ __global__ __launch_bounds__(kCountBlock) void k_count_free(const int32_t* refs,
     if (threadIdx.x == 0) counts[blockIdx.x] = s;
 }
 
-// Free slots before this thread's first one; *all: in the whole pool.
-__device__ __forceinline__ uint64_t free_before(const uint32_t* counts, uint32_t mine, uint64_t* all, uint32_t* sh) {
-    __shared__ uint64_t before_sh[kCountBlock / kWave], all_sh[kCountBlock / kWave];
+// Free slots before this thread's first one; *all: in the whole pool.  SCAN:
+// from `refs` themselves, which nobody may be writing, instead of `counts`.
+template <bool SCAN>
+__device__ __forceinline__ uint64_t free_before(const int32_t* refs, uint64_t n_slots, const uint32_t* counts,
+                                                uint32_t mine, uint64_t* all) {
+    constexpr uint32_t kBlock = SCAN ? kListBlock : kCountBlock;
+    __shared__ uint64_t before_sh[kBlock / kWave], all_sh[kBlock / kWave];
+    __shared__ uint32_t sh[kBlock / kWave];
     uint64_t before = 0, total = 0;
-    for (uint32_t b = threadIdx.x; b < gridDim.x; b += blockDim.x) {
-        const uint32_t c = counts[b];
-        total += c;
-        if (b < blockIdx.x) before += c;
+    if (SCAN) {
+        typedef int32_t Four __attribute__((ext_vector_type(4), aligned(4)));
+        const uint32_t n = (uint32_t)n_slots, full = n & ~3u, first = blockIdx.x * (kBlock * kCountPer);
+#pragma unroll 4
+        for (uint32_t i = 4 * threadIdx.x; i < full; i += 4 * kBlock) {
+            const Four v = *reinterpret_cast<const Four*>(refs + i);
+            const uint32_t c = (uint32_t)(v.x <= 0) + (v.y <= 0) + (v.z <= 0) + (v.w <= 0);
+            total += c;
+            if (i < first) before += c;
+        }
+        if (threadIdx.x < n - full) total += refs[full + threadIdx.x] <= 0;  // behind every block's first
+    } else {
+        for (uint32_t b = threadIdx.x; b < gridDim.x; b += kBlock) {
+            const uint32_t c = counts[b];
+            total += c;
+            if (b < blockIdx.x) before += c;
+        }
     }
     before = wave_sum64(before);
     total = wave_sum64(total);
@@ -189,7 +216,7 @@ __device__ __forceinline__ uint64_t free_before(const uint32_t* counts, uint32_t
     __syncthreads();
     uint64_t r = incl - mine;
     *all = 0;
-    for (uint32_t i = 0; i < kCountBlock / kWave; ++i) {
+    for (uint32_t i = 0; i < kBlock / kWave; ++i) {
         r += before_sh[i];
         *all += all_sh[i];
         if (i < w) r += sh[i];
@@ -199,14 +226,15 @@ __device__ __forceinline__ uint64_t free_before(const uint32_t* counts, uint32_t
 
 // ids[r] <- the r-th free slot, r < n.  TAKE: the slots' counts become 1, ids
 // without a slot -1, and too few free slots latch kErrFull.
-template <bool TAKE>
-__global__ __launch_bounds__(kCountBlock) void k_list_free(int32_t* refs, uint64_t n_slots, const uint32_t* counts,
-                                                           int64_t* ids, uint64_t n, uint32_t* err) {
-    __shared__ uint32_t sh[kCountBlock / kWave];
-    const uint64_t base = (uint64_t)blockIdx.x * kCountSlots + threadIdx.x * kCountPer;
+template <bool TAKE, bool SCAN>
+__global__ __launch_bounds__(SCAN ? kListBlock : kCountBlock) void k_list_free(int32_t* refs, uint64_t n_slots,
+                                                                              const uint32_t* counts, int64_t* ids,
+                                                                              uint64_t n, uint32_t* err) {
+    static_assert(!(TAKE && SCAN), "other workgroups would read counts while this one writes its own");
+    const uint64_t base = ((uint64_t)blockIdx.x * blockDim.x + threadIdx.x) * kCountPer;
     uint32_t f = free_flags(refs, n_slots, base);
     uint64_t all;
-    uint64_t r = free_before(counts, (uint32_t)__builtin_popcount(f), &all, sh);
+    uint64_t r = free_before<SCAN>(refs, n_slots, counts, (uint32_t)__builtin_popcount(f), &all);
     while (f && r < n) {
         const uint64_t slot = base + (uint32_t)__builtin_ctz(f);
         f &= f - 1;
@@ -335,11 +363,10 @@ __global__ __launch_bounds__(256) void k_pages_free(int32_t* refs, uint64_t n_sl
 __global__ __launch_bounds__(kCountBlock) void k_compact_plan(const int32_t* refs, uint64_t n_slots,
                                                               const uint32_t* counts, int64_t* map, int64_t* n_live,
                                                               uint64_t* n_moves, uint32_t* holes, uint32_t* movers) {
-    __shared__ uint32_t sh[kCountBlock / kWave];
     const uint64_t base = (uint64_t)blockIdx.x * kCountSlots + threadIdx.x * kCountPer;
     const uint32_t f = free_flags(refs, n_slots, base);
     uint64_t all;
-    uint64_t r = free_before(counts, (uint32_t)__builtin_popcount(f), &all, sh);
+    uint64_t r = free_before<false>(refs, n_slots, counts, (uint32_t)__builtin_popcount(f), &all);
     const uint64_t live = n_slots - all;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         *n_live = (int64_t)live;
@@ -418,6 +445,11 @@ static ibp_status check_page_format(ibp_meta_t h, std::initializer_list<const vo
     return IBP_OK;
 }
 
+// Threads and workgroups of a kernel that lists without counts.
+static dim3 scan_grid(uint64_t n_slots) {
+    return dim3((uint32_t)((n_slots + kListBlock * kCountPer - 1) / (kListBlock * kCountPer)));
+}
+
 static hipError_t launch_count_free(const int32_t* refs, uint64_t n_slots, uint32_t* counts, hipStream_t s) {
     hipLaunchKernelGGL(k_count_free, dim3((uint32_t)count_blocks(n_slots)), dim3(kCountBlock), 0, s, refs, n_slots,
                        counts);
@@ -476,7 +508,7 @@ ibp_status ibp_pages_alloc(ibp_meta_t h, int32_t* refs, uint64_t n_slots, int64_
     if (st != IBP_OK) return st;
     uint32_t* counts = static_cast<uint32_t*>(workspace);
     IBP_TRY(launch_count_free(refs, n_slots, counts, stream));
-    hipLaunchKernelGGL(k_list_free<true>, dim3((uint32_t)count_blocks(n_slots)), dim3(kCountBlock), 0, stream, refs,
+    hipLaunchKernelGGL((k_list_free<true, false>), dim3((uint32_t)count_blocks(n_slots)), dim3(kCountBlock), 0, stream, refs,
                        n_slots, counts, ids, n, h->d_err);
     return from_hip(hipGetLastError());
 }
@@ -502,9 +534,14 @@ ibp_status ibp_pages_fork(ibp_meta_t h, void* slots, uint64_t n_slots, uint32_t*
     if (st != IBP_OK) return st;
     uint32_t* counts = static_cast<uint32_t*>(workspace);
     int64_t* fresh = static_cast<int64_t*>(workspace) + count_words(n_slots);
-    IBP_TRY(launch_count_free(refs, n_slots, counts, stream));
-    hipLaunchKernelGGL(k_list_free<false>, dim3((uint32_t)count_blocks(n_slots)), dim3(kCountBlock), 0, stream, refs,
-                       n_slots, counts, fresh, n * n_heads, h->d_err);
+    if (n_slots <= kListSlots) {
+        hipLaunchKernelGGL((k_list_free<false, true>), scan_grid(n_slots), dim3(kListBlock), 0, stream, refs, n_slots,
+                           nullptr, fresh, n * n_heads, h->d_err);
+    } else {
+        IBP_TRY(launch_count_free(refs, n_slots, counts, stream));
+        hipLaunchKernelGGL((k_list_free<false, false>), dim3((uint32_t)count_blocks(n_slots)), dim3(kCountBlock), 0,
+                           stream, refs, n_slots, counts, fresh, n * n_heads, h->d_err);
+    }
     IBP_TRY(hipGetLastError());
     const Geo geo = make_geo(h, true, kLongTileWordsDecode);
     const ForkArgs a{static_cast<const uint8_t*>(slots), static_cast<uint8_t*>(slots), bitmask, refs, table, lens,

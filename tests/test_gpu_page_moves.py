@@ -313,3 +313,48 @@ def test_captured_fork_free_and_compact():
         for x, y in zip(eager, (a.slots, a.bm, refs, table, m, live)):
             assert torch.equal(x, y)
     assert a.check() == ibp.IBP_OK
+
+
+@pytest.mark.parametrize("n_slots", [4095, 65536, 65537, 131079])
+@pytest.mark.parametrize("at", ["front", "back", "spread"])
+def test_fork_and_compact_of_large_pools(n_slots, at):
+    """Pools on both sides of the size up to which free slots are counted and
+    listed in one launch; the counts start 4 bytes past an aligned address."""
+    T, H, B, L = 16, 2, 2, 512
+    rng = np.random.default_rng(n_slots)
+    a = Slots(n_slots, L, 32, 4096)
+    free = {"front": np.arange(6), "back": np.arange(n_slots - 6, n_slots),
+            "spread": np.sort(rng.choice(n_slots, 6, replace=False))}[at]
+    refs = np.ones(n_slots, np.int32)
+    refs[free] = 0
+    taken = rng.choice(np.flatnonzero(refs), 2 * H * B, replace=False)
+    table = np.full((4, H, B), -1, np.int64)
+    table[:2] = taken.reshape(2, H, B)
+    lens = np.array([2 * T - 1, T + 5, 0, 0], np.int32)
+    slots, bits, want_refs = a.bytes(), a.bits(), refs.copy()
+    want = fork_model(slots, bits, a.stored, want_refs, table, lens, [0, 1], [3, 2], T)
+    g_refs = torch.zeros(n_slots + 1, dtype=torch.int32, device="cuda")[1:]
+    g_refs.copy_(torch.from_numpy(refs))
+    g_table = torch.from_numpy(table.copy()).cuda()
+    ibp.ibp_pages_fork(a.meta, a.slots, n_slots, a.bm, g_refs, g_table, torch.from_numpy(lens).cuda(), ids_of([0, 1]),
+                       ids_of([3, 2]), page_tokens=T)
+    assert a.check() == ibp.IBP_OK
+    np.testing.assert_array_equal(g_table.cpu().numpy(), want)
+    np.testing.assert_array_equal(g_refs.cpu().numpy(), want_refs)
+    np.testing.assert_array_equal(a.bytes(), slots)
+    np.testing.assert_array_equal(a.bits(), bits)
+    # two free slots are left: the live pages behind them move into them
+    m = torch.empty(n_slots, dtype=torch.int64, device="cuda")
+    live = torch.empty(1, dtype=torch.int64, device="cuda")
+    ibp.ibp_pages_compact(a.meta, a.slots, n_slots, a.bm, g_refs, m, live, table=g_table)
+    assert a.check() == ibp.IBP_OK and int(live) == n_slots - 2
+    new = np.where(want_refs > 0, np.arange(n_slots), -1)
+    holes = [i for i in np.flatnonzero(want_refs == 0) if i < n_slots - 2]
+    movers = [i for i in (n_slots - 1, n_slots - 2) if want_refs[i] > 0]
+    assert len(holes) == len(movers)
+    for d, s in zip(holes, movers):
+        new[s] = d
+        want_refs[d], want_refs[s] = want_refs[s], 0
+    np.testing.assert_array_equal(m.cpu().numpy(), new)
+    np.testing.assert_array_equal(g_refs.cpu().numpy(), want_refs)
+    np.testing.assert_array_equal(g_table.cpu().numpy(), np.where(want >= 0, new[want], -1))
