@@ -394,7 +394,8 @@ ibp_status ibp_tree_attention(const ibp_pages* k, const ibp_pages* v, const ibp_
 /* Bounds of pages: for i < n, bounds[ids[i]] (2 x head_dim numbers of the
  * data's type) <- the smallest, then the largest, of each number over the
  * first tokens[i] tokens (NULL: all) of page ids[i]; an id of -1 or no token
- * at all is skipped, and a NaN is passed on.  With q these bound the score of
+ * at all is skipped, and a NaN is passed on.  An id may be listed twice with
+ * the same tokens only.  With q these bound the score of
  * every key in the page: sum over d of max(q_d lo_d, q_d hi_d). */
 ibp_status ibp_page_bounds(const ibp_pages* k, uint32_t dtype, uint32_t head_dim, const int64_t* ids,
                            const int32_t* tokens, uint64_t n, void* bounds, hipStream_t stream);

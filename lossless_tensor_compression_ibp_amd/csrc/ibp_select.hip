@@ -274,7 +274,9 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
                             // a NaN is left out: fmaxf takes its other argument
                             v[i] = (heads[c] >> i) & 1u ? fmaxf(s[i], -__builtin_inff()) : -__builtin_inff();
                             w[i] = wp[i] - wm[i];
-                            w[i] = w[i] < __builtin_inff() ? w[i] : 0.f;
+                            // (a NaN is a NaN in 64 bits too; an infinite sum may be
+                            // an overflow of 32 bits and makes every page near)
+                            w[i] = fmaxf(w[i], 0.f);
                         }
                         if (a.pad >= 4) {
                             float m = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
@@ -592,12 +594,16 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
         });
         const float t_lo = value_of(lo + (bin << drop));
         const float t_hi = value_of(min(hi, lo + (bin << drop) + ((1u << drop) - 1)));
-        if (t_lo - t_lo == 0.f && t_hi - t_hi == 0.f && slack > 0.f) {
+        if (slack > 0.f) {
             // Every true score is within `slack` of its sum, so the want-th
             // largest true one lies between t_lo and t_hi widened by slack;
             // pages that are further than two of them outside are decided
             // (a third covers the roundings of these bounds and of the score).
-            const uint32_t near_lo = order_of(t_lo - 3.f * slack), near_hi = order_of(t_hi + 3.f * slack);
+            // An infinite slack (the products overflow 32 bits, or bounds are
+            // infinite) decides none.
+            const bool bounded = slack < __builtin_inff();
+            const uint32_t near_lo = order_of(bounded ? t_lo - 3.f * slack : -__builtin_inff());
+            const uint32_t near_hi = order_of(bounded ? t_hi + 3.f * slack : __builtin_inff());
             uint32_t n_above = 0, n_near = 0;
             own([&](uint32_t b, uint32_t k) __attribute__((always_inline)) {
                 if (k > near_hi) {
@@ -672,7 +678,7 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
                 }
             }
         } else {
-            // no slack (all products zero, or not finite): the sums as they are
+            // no slack (all products zero, or NaN): the sums as they are
             cut = nth_largest(want, lo, hi, sh, turn, &above, own_keys);
             ties = want - above;
         }
@@ -773,8 +779,8 @@ ibp_status ibp_page_bounds(const ibp_pages* k, uint32_t dtype, uint32_t head_dim
         constexpr int NV = decltype(nv)::value;
         const uint64_t stage = 4ull * kBoundWaves * page_stage_words<NV>();
         // tables that leave no room for a second workgroup on a compute unit
-        // stay in device memory
-        const bool lds = pool.Mw < 4 || tab + stage <= kLdsPerCu / 2;
+        // (and none in the LDS that a launch has by itself) stay in device memory
+        const bool lds = pool.Mw < 4 || tab + stage <= kMaxLdsPerBlock;
         const uint64_t waves = std::min<uint64_t>(n, 4ull * kBoundWaves * 4 * h->cu_count);
         const dim3 grid((uint32_t)((waves + kBoundWaves - 1) / kBoundWaves));
         if (lds)

@@ -50,6 +50,31 @@ def test_bounds_pass_on_nan_and_infinity():
     assert torch.equal(b[ok], want[ok])
 
 
+@pytest.mark.parametrize("runs", [3, 4, 5, 7, 8])
+def test_bounds_with_large_tables(runs):
+    """Tables of 1,024 words from just below to just above what a launch's LDS
+    holds."""
+    page, dim, n = 32, 128, 200
+    L = page * dim * 2
+    bits = np.uint32(sum(1 << b for b in (1, 5, 9, 13, 17, 21, 25)[:runs - 1]))
+    mask = np.full(L // 4 // 2, bits, np.uint32)
+    mask[77] = 0
+    x = values(n, page, dim, torch.bfloat16, runs)
+    words = x.view(torch.int32).reshape(n, -1)
+    keep = torch.from_numpy((~np.tile(mask, 2)).view(np.int32)).cuda()
+    words[::2] &= keep
+    p = Pool(x, None)
+    p.meta = ibp.ibp_meta_create(L, 32, 4 * L, mask, np.zeros_like(mask))
+    assert ibp.ibp_meta_get_info(p.meta)["max_runs"] == runs
+    ibp.ibp_compress(p.meta, x.view(torch.uint8).reshape(n, L), n, p.slots, p.bitmask)
+    p.pages = ibp.Pages(p.meta, p.slots, n, p.bitmask)
+    assert p.compressed().any()
+    b = torch.zeros(n, 2, dim, dtype=x.dtype, device="cuda")
+    ibp.ibp_page_bounds(p.pages, torch.arange(n, device="cuda"), None, b)
+    assert p.check() == ibp.IBP_OK
+    assert torch.equal(b[:, 0], x.amin(1)) and torch.equal(b[:, 1], x.amax(1))
+
+
 def test_bounds_errors():
     p = Pool(values(8, 16, 64, torch.bfloat16, 1))
     b = torch.zeros(8, 2, 64, dtype=torch.bfloat16, device="cuda")
@@ -157,6 +182,33 @@ def test_select_near_scores_are_summed_in_64_bits():
 
     q = torch.ones(2, 4, 128, device="cuda", dtype=torch.bfloat16)
     select_case([4000, 3333], [4000, 3333], 4, 2, 128, 16, 25, 1, 2, make=close, q=q, seed=3)
+
+
+@pytest.mark.parametrize("rows", [2, 9])
+@pytest.mark.parametrize("n", [300, 2000, 9000])
+def test_select_sums_that_overflow_32_bits(rows, n):
+    """Products of 2e38 that cancel: 32-bit sums are infinite or NaN where those
+    of 64 bits are not; and scores that are infinite in both."""
+    def large(b):
+        b = b * 1e17
+        b[:, :, 0], b[:, :, 1], b[:, :, 2], b[:, :, 3] = 2e19, 1.5e19, -2e19, -1.5e19
+        b[::len(b) // 12, 1, 9] = 3e38  # times q: more than 32 bits hold
+        return b
+
+    q = torch.ones(rows, 2, 64, device="cuda", dtype=torch.bfloat16) * 1e19
+    q[:, 1] *= 0.5
+    select_case([16 * n - 1] * rows, [16 * n] * 2, 2, 1, 64, 16, 40, 1, 2, make=large, q=q, seed=n,
+                row_seq=[i % 2 for i in range(rows)])
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf])
+def test_select_infinite_bounds(bad):
+    def some(b):
+        b = b.clone()
+        b[::3, :, 3] = bad
+        return b
+
+    select_case([1600, 900], [1600, 900], 4, 1, 64, 16, 60, 0, 1, make=some, seed=8)
 
 
 def test_select_nan_ranks_last():
