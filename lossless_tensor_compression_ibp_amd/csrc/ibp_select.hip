@@ -114,12 +114,21 @@ __global__ __launch_bounds__(kWave * kBoundWaves) void k_page_bounds(Pool pool, 
 // lanes of a page for larger ones.  Groups are padded to `pad` heads (1, 2, 4,
 // 8 or a multiple of 16), so that no group straddles tiles.
 //
-// A wave takes 64 blocks of one head for CT tiles of columns, the next 16
-// pages' bounds in flight while it multiplies.  Decoding, where every row has
-// pages of its own, takes CT = 1 and other blocks in every wave, and is bound
-// by the bounds' bytes.  Where rows share a sequence the four waves of a
-// workgroup take the same blocks for different rows, so that three of them
-// find the bounds in the compute unit's cache.
+// A wave takes 64 blocks of one head for CT tiles of columns.
+//   k_scores, decoding, where every row has pages of its own: CT = 1, other
+//     blocks in every wave, operands straight from memory.  Bound by the
+//     bounds' bytes (16 rows of 2,048 blocks by 8 heads of 128 dims, 134 MB:
+//     20.7 us, 6.5 TB/s out of the last-level cache).
+//   k_scores_shared, rows that share a sequence: the four waves of a workgroup
+//     take the same blocks for rows of their own, and bring the bounds to LDS
+//     once.  An operand's 16 lanes are 16 pages, so that a load from memory
+//     takes the cache 64 lookups instead of 8: read that way, with each wave
+//     on its own, the cache's one lookup per cycle was the limit (512 rows of
+//     4,096 blocks by 8 heads of 128 dims: 138 us, 79.6 through LDS, of which
+//     the matrix cores work 27).  Workgroups whose rows belong to several
+//     sequences, and 256 dims, which LDS has no room for, still read that way.
+// Heads are the fastest index of the grid, so that with eight of them each
+// XCD's L2 holds the bounds of one (decoding: 22.6 us otherwise).
 // ---------------------------------------------------------------------------
 struct SelectArgs {
     const void* q;
@@ -140,7 +149,6 @@ struct SelectArgs {
     uint32_t head_tiles;     // column tiles of one row (pad / 16, or 1)
     uint32_t wave_rows;      // rows of one wave
     uint32_t span;           // times 64 blocks per wave
-    uint32_t same_blocks;    // a workgroup's waves take the same blocks, and rows of their own
 };
 
 constexpr uint32_t kScoreWaves = 4;
@@ -160,9 +168,26 @@ __device__ __forceinline__ uint32_t row_blocks(const SelectArgs& a, uint64_t r, 
     return (uint32_t)(nb < a.blocks ? nb : a.blocks);
 }
 
-// One wave: rows r0 .. of head h, blocks b_first .. of a.span * 64.
-template <class E, int D, int CT>
-__device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, uint32_t h, uint32_t b_first) {
+// The bounds of 64 blocks in LDS, rows padded so that 16 blocks' operands
+// spread over all banks.
+template <int D>
+struct BoundTile {
+    static constexpr uint32_t stride = 4 * D + 16, bytes = kWaveBlocks * stride;
+    static constexpr bool fits = D <= 128;
+};
+
+// Of a workgroup whose waves' rows all belong to one sequence: that sequence
+// and its most blocks (`tile` as well, else NULL).
+struct Together {
+    char* tile;
+    uint32_t seq, nb;
+};
+
+// One wave: rows r0 .. of head h, blocks b_first .. of a.span * 64.  STAGED:
+// the whole workgroup, which brings the bounds to LDS 64 blocks at a time.
+template <class E, int D, int CT, bool ONE_ROW, bool STAGED>
+__device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, uint32_t h, uint32_t b_first,
+                                             const Together wg = {}) {
     using V8 = typename E::V8;
     constexpr int DK = D / 32;
     const uint32_t lane = lane_id();
@@ -172,13 +197,15 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
     uint32_t my_nb = 0;
     if (lane < a.wave_rows && r0 + lane < a.n_rows) my_nb = row_blocks(a, r0 + lane, &my_seq);
     uint64_t todo = ballot(my_nb > b_first);
-    while (todo) {  // one sequence after another; usually there is one
-        const uint32_t lead = (uint32_t)__builtin_ctzll(todo);
-        const uint32_t seq = lane_value((uint32_t)my_seq, (int)lead);
+    bool first_turn = STAGED;
+    while (todo || first_turn) {  // one sequence after another; usually there is one
+        first_turn = false;
+        const uint32_t seq = STAGED ? wg.seq : lane_value((uint32_t)my_seq, (int)__builtin_ctzll(todo));
         const uint64_t mine = todo & ballot((uint32_t)my_seq == seq && my_nb > b_first);
         todo &= ~mine;
-        uint32_t nb = 0;
-        for (uint64_t m = mine; m; m &= m - 1) nb = max(nb, lane_value(my_nb, (int)__builtin_ctzll(m)));
+        uint32_t nb = wg.nb;
+        if (!STAGED)
+            for (uint64_t m = mine; m; m &= m - 1) nb = max(nb, lane_value(my_nb, (int)__builtin_ctzll(m)));
         // 64 page ids at once
         auto ids_at = [&](uint32_t b) __attribute__((always_inline)) -> uint32_t {
             if (b + lane >= nb) return kNoPage;
@@ -215,7 +242,8 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
             }
             // of columns 4 g + i of each tile: which hold a head, the row of
             // the first, and the blocks of each row they belong to
-            uint32_t heads[CT], row_nb[CT][4];
+            constexpr int ROWS = ONE_ROW ? 1 : 4;
+            uint32_t heads[CT], row_nb[CT][ROWS];
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 heads[c] = 0;
@@ -224,9 +252,11 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t row = (x0 + i) >> a.log2_pad;
                     if (x0 + i - (row << a.log2_pad) < a.group) heads[c] |= 1u << i;
-                    const bool live = row < a.wave_rows && ((mine >> (row & 63u)) & 1u);
-                    const uint32_t n = (uint32_t)__shfl((int)my_nb, (int)(row & 63u));
-                    row_nb[c][i] = live ? n : 0u;
+                    if (i < ROWS) {
+                        const bool live = row < a.wave_rows && ((mine >> (row & 63u)) & 1u);
+                        const uint32_t n = (uint32_t)__shfl((int)my_nb, (int)(row & 63u));
+                        row_nb[c][i] = live ? n : 0u;
+                    }
                 }
             }
             uint32_t id_next = ids_at(b_first);
@@ -234,38 +264,62 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
                 const uint32_t id = id_next;
                 id_next = b0 + kWaveBlocks < b_end ? ids_at(b0 + kWaveBlocks) : kNoPage;
                 const uint32_t tiles = min((b_end - b0 + 15) / 16, kWaveBlocks / 16);
-                V8 lo[DK], hi[DK], lo_next[DK], hi_next[DK];
-                auto fetch = [&](uint32_t t) __attribute__((always_inline)) {
-                    const uint32_t pid = (uint32_t)__shfl((int)id, (int)(16 * t + col));
-                    const char* base =
-                        static_cast<const char*>(a.bounds) + (uint64_t)(pid == kNoPage ? 0u : pid) * (4ull * D) + 16 * g;
+                if constexpr (STAGED) {
+                    // a wave brings 16 blocks, each lane 16 bytes at a time
+                    constexpr uint32_t PIECES = D / 4, AT_ONCE = kWave / PIECES;
+                    const uint32_t wib = uniform(threadIdx.x / kWave);
+                    u32x4 piece[16 / AT_ONCE];
 #pragma unroll
-                    for (int kk = 0; kk < DK; ++kk) {
-                        lo_next[kk] = *reinterpret_cast<const V8*>(base + 64 * kk);
-                        hi_next[kk] = *reinterpret_cast<const V8*>(base + 2 * D + 64 * kk);
+                    for (uint32_t i = 0; i < 16 / AT_ONCE; ++i) {
+                        const uint32_t pid = (uint32_t)__shfl((int)id, (int)(16 * wib + AT_ONCE * i + lane / PIECES));
+                        piece[i] = *reinterpret_cast<const u32x4*>(
+                            static_cast<const char*>(a.bounds) + (uint64_t)(pid == kNoPage ? 0u : pid) * (4ull * D) +
+                            16 * (lane % PIECES));
                     }
-                };
-                fetch(0);
+                    __syncthreads();  // the 64 blocks before have been read
+#pragma unroll
+                    for (uint32_t i = 0; i < 16 / AT_ONCE; ++i)
+                        *reinterpret_cast<u32x4*>(wg.tile + (16 * wib + AT_ONCE * i + lane / PIECES) * BoundTile<D>::stride +
+                                                  16 * (lane % PIECES)) = piece[i];
+                    __syncthreads();
+                }
                 float slack[CT];
 #pragma unroll
                 for (int c = 0; c < CT; ++c) slack[c] = 0.f;
+#pragma unroll 1
                 for (uint32_t t = 0; t < tiles; ++t) {
-#pragma unroll
-                    for (int kk = 0; kk < DK; ++kk) {
-                        lo[kk] = lo_next[kk];
-                        hi[kk] = hi_next[kk];
-                    }
-                    if (t + 1 < tiles) fetch(t + 1);
-#pragma unroll
-                    for (int c = 0; c < CT; ++c) {
-                        f32x4 s = {0.f, 0.f, 0.f, 0.f}, wp = s, wm = s;
+                    V8 lo[DK], hi[DK];
+                    auto read = [&](const char* base) __attribute__((always_inline)) {
 #pragma unroll
                         for (int kk = 0; kk < DK; ++kk) {
-                            s = E::mfma(qp[c][kk], hi[kk], s);
-                            s = E::mfma(qm[c][kk], lo[kk], s);
-                            wp = E::mfma(qp[c][kk], bits_as<V8>(bits_as<u32x4>(hi[kk]) & 0x7FFF7FFFu), wp);
-                            wm = E::mfma(qm[c][kk], bits_as<V8>(bits_as<u32x4>(lo[kk]) & 0x7FFF7FFFu), wm);
+                            lo[kk] = *reinterpret_cast<const V8*>(base + 64 * kk);
+                            hi[kk] = *reinterpret_cast<const V8*>(base + 2 * D + 64 * kk);
                         }
+                    };
+                    if constexpr (STAGED) {
+                        read(wg.tile + (16 * t + col) * BoundTile<D>::stride + 16 * g);
+                    } else {
+                        const uint32_t pid = (uint32_t)__shfl((int)id, (int)(16 * t + col));
+                        read(static_cast<const char*>(a.bounds) + (uint64_t)(pid == kNoPage ? 0u : pid) * (4ull * D) +
+                             16 * g);
+                    }
+                    f32x4 sum[CT], sum_p[CT], sum_m[CT];
+#pragma unroll
+                    for (int kk = 0; kk < DK; ++kk) {
+                        const V8 hi_abs = bits_as<V8>(bits_as<u32x4>(hi[kk]) & 0x7FFF7FFFu);
+                        const V8 lo_abs = bits_as<V8>(bits_as<u32x4>(lo[kk]) & 0x7FFF7FFFu);
+#pragma unroll
+                        for (int c = 0; c < CT; ++c) {
+                            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                            sum[c] = E::mfma(qp[c][kk], hi[kk], kk ? sum[c] : zero);
+                            sum_p[c] = E::mfma(qp[c][kk], hi_abs, kk ? sum_p[c] : zero);
+                            sum_m[c] = E::mfma(qm[c][kk], lo_abs, kk ? sum_m[c] : zero);
+                            sum[c] = E::mfma(qm[c][kk], lo[kk], sum[c]);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) {
+                        const f32x4 s = sum[c], wp = sum_p[c], wm = sum_m[c];
                         const uint32_t x0 = (ct0 + c) * 16 + 4 * g, row0 = x0 >> a.log2_pad;
                         const uint32_t b = b0 + 16 * t + col;
                         float v[4], w[4];
@@ -278,7 +332,7 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
                             // an overflow of 32 bits and makes every page near)
                             w[i] = fmaxf(w[i], 0.f);
                         }
-                        if (a.pad >= 4) {
+                        if constexpr (ONE_ROW) {
                             float m = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
                             float e = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
                             if (a.pad >= 8) {
@@ -321,7 +375,7 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
                     for (int o = 1; o < 16; o <<= 1) e = fmaxf(e, __shfl_xor(e, o));
                     const uint32_t x0 = (ct0 + c) * 16 + 4 * g;
 #pragma unroll
-                    for (uint32_t i = 0; i < 4; ++i) {
+                    for (uint32_t i = 0; i < (uint32_t)ROWS; ++i) {
                         const uint32_t row = (x0 + i) >> a.log2_pad;
                         const bool first = a.head_tiles > 1 ? g == 0 && i == 0 : x0 + i == (row << a.log2_pad);
                         if (col == 0 && first && row_nb[c][i] > b0) {
@@ -336,15 +390,52 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
     }
 }
 
-template <class E, int D, int CT>
+template <class E, int D, int CT, bool ONE_ROW>
 __global__ __launch_bounds__(kWave * kScoreWaves, 2) void k_scores(SelectArgs a) {
     const uint32_t wib = uniform(threadIdx.x / kWave);
-    if (a.same_blocks)
-        score_blocks<E, D, CT>(a, ((uint64_t)blockIdx.z * kScoreWaves + wib) * a.wave_rows, blockIdx.y,
-                               blockIdx.x * kWaveBlocks * a.span);
-    else
-        score_blocks<E, D, CT>(a, (uint64_t)blockIdx.z * a.wave_rows, blockIdx.y,
-                               (blockIdx.x * kScoreWaves + wib) * kWaveBlocks * a.span);
+    score_blocks<E, D, CT, ONE_ROW, false>(a, (uint64_t)blockIdx.z * a.wave_rows, blockIdx.x,
+                                           (blockIdx.y * kScoreWaves + wib) * kWaveBlocks * a.span);
+}
+
+template <class E, int D, int CT, bool ONE_ROW>
+__global__ __launch_bounds__(kWave * kScoreWaves, D == 128 && ONE_ROW ? 3 : 2) void k_scores_shared(SelectArgs a) {
+    const uint32_t lane = lane_id(), wib = uniform(threadIdx.x / kWave);
+    const uint64_t r0 = ((uint64_t)blockIdx.z * kScoreWaves + wib) * a.wave_rows;
+    const uint32_t b_first = blockIdx.y * kWaveBlocks * a.span;
+    if constexpr (BoundTile<D>::fits) {
+        __shared__ __align__(16) char tile[BoundTile<D>::bytes];
+        __shared__ uint32_t seq_sh[kScoreWaves], nb_sh[kScoreWaves], mixed_sh[kScoreWaves];
+        int64_t seq = -1;
+        uint32_t nb = 0;
+        if (lane < a.wave_rows && r0 + lane < a.n_rows) nb = row_blocks(a, r0 + lane, &seq);
+        const uint64_t on = ballot(nb > b_first);
+        const uint32_t lead = on ? (uint32_t)__builtin_ctzll(on) : 0u;
+        const uint32_t wave_seq = lane_value((uint32_t)seq, (int)lead);
+        const uint64_t others = ballot(nb > b_first && (uint32_t)seq != wave_seq);
+        for (int o = 32; o > 0; o >>= 1) nb = max(nb, (uint32_t)__shfl_xor((int)nb, o));
+        if (lane == 0) {
+            seq_sh[wib] = wave_seq;
+            nb_sh[wib] = on ? nb : 0u;
+            mixed_sh[wib] = others != 0;
+        }
+        __syncthreads();
+        Together wg{tile, 0, 0};
+        bool mixed = false;
+        for (uint32_t w = 0; w < kScoreWaves; ++w) {
+            if (!nb_sh[w]) continue;
+            mixed = mixed || mixed_sh[w] || (wg.nb && seq_sh[w] != wg.seq);
+            wg.seq = seq_sh[w];
+            wg.nb = max(wg.nb, nb_sh[w]);
+        }
+        wg.seq = uniform(wg.seq);
+        wg.nb = uniform(wg.nb);
+        if (wg.nb == 0) return;
+        if (!mixed) {
+            score_blocks<E, D, CT, ONE_ROW, true>(a, r0, blockIdx.x, b_first, wg);
+            return;
+        }
+    }
+    score_blocks<E, D, CT, ONE_ROW, false>(a, r0, blockIdx.x, b_first);
 }
 
 // ---------------------------------------------------------------------------
@@ -718,8 +809,8 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
 }
 
 // 64 registers for pages of up to 128 dims, so that eight waves fit a SIMD: the
-// 64-bit sums read from everywhere and wait (2,048 rows of 512 blocks on 8
-// heads: 91 us, 124 us with the 94 registers the compiler takes by itself).
+// 64-bit sums read from everywhere and wait (512 rows of 4,096 blocks on 8
+// heads: 88 us, 124 us with the 94 registers the compiler takes by itself).
 // 256 dims would spill.
 template <class E, int D, bool KEYS>
 __global__ __launch_bounds__(1024, D <= 128 ? 8 : 4) void k_choose(SelectArgs a) {
@@ -743,7 +834,7 @@ __global__ __launch_bounds__(kWave * kSelectWaves) void k_select(SelectArgs a) {
     const uint32_t h = blockIdx.x % a.kv_heads;
 #pragma unroll 1
     for (uint32_t b = uniform(threadIdx.x / kWave) * kWaveBlocks; b < a.blocks; b += kSelectWaves * kWaveBlocks)
-        score_blocks<E, D, 1>(a, r, h, b);
+        score_blocks<E, D, 1, true, false>(a, r, h, b);
     __threadfence_block();
     __syncthreads();
     choose_blocks<E, D, true>(a, sh, smem);
@@ -852,24 +943,25 @@ ibp_status ibp_select_pages(ibp_meta_t h, const ibp_attention* a, const void* q,
     s.keep_first = keep_first;
     s.keep_last = keep_last;
     s.n_out = n_blocks;
-    s.pad = 1;
+    // Many rows per sequence share the pages' bounds, two tiles of rows a wave
+    // (one of 256 dims, for the registers); few rows take a wave each, whose
+    // lanes then always hold columns of one row.
+    const bool shared = a->n_rows >= 4 * a->n_seqs && s.group <= 16;
+    s.pad = shared ? 1 : 4;
     while (s.pad < s.group && s.pad < 16) s.pad *= 2;
     if (s.group > 16) s.pad = (s.group + 15) / 16 * 16;
     s.log2_pad = s.pad > 16 ? 31 : (uint32_t)__builtin_ctz(s.pad);
     s.rows_per_tile = s.pad < 16 ? 16 / s.pad : 1;
     s.head_tiles = s.pad > 16 ? s.pad / 16 : 1;
-    // Many rows per sequence share the pages' bounds, two tiles of rows a wave
-    // (one of 256 dims, for the registers); few rows take a wave each.
-    const bool shared = a->n_rows >= 4 * a->n_seqs && s.head_tiles == 1;
     const uint32_t ct = shared && a->head_dim <= 128 ? 2 : 1;
-    s.same_blocks = shared;
     s.wave_rows = shared ? ct * s.rows_per_tile : 1;
-    // A wave that shares pays for its queries once: as many blocks as leave
-    // about 1,024 workgroups.  (512 rows by 4,096 blocks by 8 heads of 128
-    // dims: 201 us with 64 blocks per wave.)
+    // A wave that shares pays for its queries once: as many blocks as give one
+    // round of workgroups, three on a compute unit of 256.  (512 rows by 4,096
+    // blocks by 8 heads of 128 dims, read without LDS: 136 us in 768 workgroups,
+    // 162 in 1,024, 156 in 2,048.)
     const uint64_t row_groups = (a->n_rows + ct * s.rows_per_tile * kScoreWaves - 1) / (ct * s.rows_per_tile * kScoreWaves);
     const uint64_t all_chunks = row_groups * a->n_kv_heads * select_chunks(a);
-    s.span = shared ? (uint32_t)std::min<uint64_t>(std::max<uint64_t>(1, all_chunks / 1024), 64) : 1;
+    s.span = shared ? (uint32_t)std::min<uint64_t>(std::max<uint64_t>(1, (all_chunks + 767) / 768), 64) : 1;
     const uint64_t per_wg_rows = (uint64_t)s.wave_rows * (shared ? kScoreWaves : 1);
     const uint64_t groups = (a->n_rows + per_wg_rows - 1) / per_wg_rows;
     if (groups > 65535 || a->n_kv_heads > 65535 || a->n_rows * a->n_kv_heads > 0x7FFFFFFFull)
@@ -887,11 +979,18 @@ ibp_status ibp_select_pages(ibp_meta_t h, const ibp_attention* a, const void* q,
         }
         if (scored) {  // no row can have more pages than it may read otherwise
             const uint64_t per_wg = (uint64_t)(shared ? 1 : kScoreWaves) * kWaveBlocks * s.span;
-            const dim3 tiles((uint32_t)((a->table_blocks + per_wg - 1) / per_wg), a->n_kv_heads, (uint32_t)groups);
+            const dim3 tiles(a->n_kv_heads, (uint32_t)((a->table_blocks + per_wg - 1) / per_wg), (uint32_t)groups);
+            auto by_rows = [&](auto ct_tiles, dim3 g) {
+                constexpr int CT = decltype(ct_tiles)::value;
+                if (s.pad >= 4)
+                    hipLaunchKernelGGL((k_scores_shared<E, D, CT, true>), g, dim3(kWave * kScoreWaves), 0, stream, s);
+                else
+                    hipLaunchKernelGGL((k_scores_shared<E, D, CT, false>), g, dim3(kWave * kScoreWaves), 0, stream, s);
+            };
             if (shared)
-                hipLaunchKernelGGL((k_scores<E, D, D == 256 ? 1 : 2>), tiles, dim3(kWave * kScoreWaves), 0, stream, s);
+                by_rows(std::integral_constant<int, D == 256 ? 1 : 2>{}, tiles);
             else
-                hipLaunchKernelGGL((k_scores<E, D, 1>), tiles, dim3(kWave * kScoreWaves), 0, stream, s);
+                hipLaunchKernelGGL((k_scores<E, D, 1, true>), tiles, dim3(kWave * kScoreWaves), 0, stream, s);
             const hipError_t err = hipGetLastError();
             if (err != hipSuccess) return err;
         }

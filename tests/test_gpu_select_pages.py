@@ -158,6 +158,20 @@ def test_select_rows_of_several_sequences():
     select_case(lens, seqs, 4, 2, 128, 16, 9, 1, 2, seed=5, row_seq=row_seq)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 2, 4, 7, 16])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_select_many_rows_of_a_sequence(dim, group, mixed):
+    """Rows that share their pages' bounds: blocks of rows of one sequence, and
+    rows of two in any order, with lengths from nothing to all of it."""
+    seqs = [3300, 1500]
+    rng = np.random.default_rng(dim + group)
+    row_seq = rng.integers(0, 2, 37).tolist() if mixed else [0] * 24 + [1] * 13
+    lens = [int(rng.integers(0, seqs[s] + 1)) for s in row_seq]
+    lens[0], lens[5], lens[36] = seqs[row_seq[0]], 0, 1
+    select_case(lens, seqs, 2 * group, 2, dim, 16, 11, 1, 2, seed=dim, row_seq=row_seq)
+
+
 def test_select_ties_go_to_the_lower_block():
     def same(b):
         return b[:1].expand_as(b).contiguous()
