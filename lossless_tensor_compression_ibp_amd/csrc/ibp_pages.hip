@@ -40,10 +40,13 @@ constexpr uint32_t kCountSlots = kCountBlock * kCountPer;
 // read all counts, at most 16 loads of 16 bytes per thread.  With 32,768 slots
 // that is 6.7 us on the GPU against 5.4 in two launches, but forks are bound by
 // the host, for which a launch is 4 to 5 us (fork and free 28.8 us, 34.3 with
-// the second launch).  The plan of a compaction, bound by the GPU, took 10.4 us
-// this way with 65,536 slots and 6.8 in two launches, which it keeps.
+// the second launch).  The plan of a compaction does so in pools of up to
+// kPlanSlots (pools of a few thousand slots, bound by the host: 27 us a call,
+// 30 with the second launch); with 65,536 slots, where the GPU is the bound, it
+// took 10.4 us this way and 6.8 in two launches.
 constexpr uint32_t kListBlock = 1024;
 constexpr uint64_t kListSlots = 65536;
+constexpr uint64_t kPlanSlots = 32768;
 
 // Removed bits of the item's header, summed over the wave.  st[0] of lane l
 // holds words 4 l .. 4 l + 3 of the slot, which include every header word
@@ -365,13 +368,14 @@ __global__ __launch_bounds__(256) void k_pages_free(int32_t* refs, uint64_t n_sl
 // counted from the back): as many movers as holes, and a mover lies behind
 // every hole, so no move reads a slot that another one writes.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(kCountBlock) void k_compact_plan(const int32_t* refs, uint64_t n_slots,
-                                                              const uint32_t* counts, int64_t* map, int64_t* n_live,
-                                                              uint64_t* n_moves, uint32_t* holes, uint32_t* movers) {
-    const uint64_t base = (uint64_t)blockIdx.x * kCountSlots + threadIdx.x * kCountPer;
+template <bool SCAN>
+__global__ __launch_bounds__(SCAN ? kListBlock : kCountBlock) void k_compact_plan(
+    const int32_t* refs, uint64_t n_slots, const uint32_t* counts, int64_t* map, int64_t* n_live, uint64_t* n_moves,
+    uint32_t* holes, uint32_t* movers) {
+    const uint64_t base = ((uint64_t)blockIdx.x * blockDim.x + threadIdx.x) * kCountPer;
     const uint32_t f = free_flags(refs, n_slots, base);
     uint64_t all;
-    uint64_t r = free_before<false>(refs, n_slots, counts, (uint32_t)__builtin_popcount(f), &all);
+    uint64_t r = free_before<SCAN>(refs, n_slots, counts, (uint32_t)__builtin_popcount(f), &all);
     const uint64_t live = n_slots - all;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         *n_live = (int64_t)live;
@@ -596,9 +600,14 @@ ibp_status ibp_pages_compact(ibp_meta_t h, void* slots, uint64_t n_slots, uint32
     uint64_t* n_moves = static_cast<uint64_t*>(workspace) + count_words(n_slots);
     uint32_t* holes = reinterpret_cast<uint32_t*>(n_moves + 1);
     uint32_t* movers = holes + n_slots;
-    IBP_TRY(launch_count_free(refs, n_slots, counts, stream));
-    hipLaunchKernelGGL(k_compact_plan, dim3((uint32_t)count_blocks(n_slots)), dim3(kCountBlock), 0, stream, refs,
-                       n_slots, counts, map, n_live, n_moves, holes, movers);
+    if (n_slots <= kPlanSlots) {
+        hipLaunchKernelGGL(k_compact_plan<true>, scan_grid(n_slots), dim3(kListBlock), 0, stream, refs, n_slots,
+                           nullptr, map, n_live, n_moves, holes, movers);
+    } else {
+        IBP_TRY(launch_count_free(refs, n_slots, counts, stream));
+        hipLaunchKernelGGL(k_compact_plan<false>, dim3((uint32_t)count_blocks(n_slots)), dim3(kCountBlock), 0, stream,
+                           refs, n_slots, counts, map, n_live, n_moves, holes, movers);
+    }
     IBP_TRY(hipGetLastError());
     const Geo geo = make_geo(h, true, kLongTileWordsDecode);
     // at most half of the pool moves

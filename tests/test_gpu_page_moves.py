@@ -315,10 +315,10 @@ def test_captured_fork_free_and_compact():
     assert a.check() == ibp.IBP_OK
 
 
-@pytest.mark.parametrize("n_slots", [4095, 65536, 65537, 131079])
+@pytest.mark.parametrize("n_slots", [4095, 32768, 32769, 65536, 65537, 131079])
 @pytest.mark.parametrize("at", ["front", "back", "spread"])
 def test_fork_and_compact_of_large_pools(n_slots, at):
-    """Pools on both sides of the size up to which free slots are counted and
+    """Pools on both sides of the sizes up to which free slots are counted and
     listed in one launch; the counts start 4 bytes past an aligned address."""
     T, H, B, L = 16, 2, 2, 512
     rng = np.random.default_rng(n_slots)
