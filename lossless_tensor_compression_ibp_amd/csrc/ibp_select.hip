@@ -592,8 +592,9 @@ __device__ __forceinline__ uint32_t exact_key(const SelectArgs& a, uint64_t r, u
                 for (int e = 0; e < 8; ++e) {
                     const int sh = 16 * (e & 1);
                     const double y = (double)E::from_bits(x[e >> 1] >> sh);
-                    s += (y > 0.0 ? y : 0.0) * (double)E::from_bits(hi[e >> 1] >> sh) +
-                         (y < 0.0 ? y : 0.0) * (double)E::from_bits(lo[e >> 1] >> sh);
+                    // (a NaN stays in both halves)
+                    s += (y < 0.0 ? 0.0 : y) * (double)E::from_bits(hi[e >> 1] >> sh) +
+                         (y > 0.0 ? 0.0 : y) * (double)E::from_bits(lo[e >> 1] >> sh);
                 }
             }
         }
