@@ -408,7 +408,8 @@ ibp_status ibp_page_bounds(const ibp_pages* k, uint32_t dtype, uint32_t head_dim
  * with the highest score until there are n_blocks.  A block's score is the
  * highest of its bound over the query heads of the group, summed in 64 bits
  * and rounded to 32; equal scores go to the lower block, and a NaN counts as
- * the lowest.  bounds: pool-wide, as ibp_page_bounds leaves them, indexed by
+ * the lowest (an infinite bound is one like any other: only 0 times infinity
+ * and sums of both infinities are NaN).  bounds: pool-wide, as ibp_page_bounds leaves them, indexed by
  * the ids of the keys' table.  At most 2^17 blocks per row.  Of a, max_len,
  * max_new, scale and the new_ strides are not read. */
 uint64_t ibp_select_pages_workspace(const ibp_attention* a);

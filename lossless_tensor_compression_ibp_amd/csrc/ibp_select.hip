@@ -2,8 +2,10 @@
 // the keys, and the choice of the pages with the highest bound on the score.
 //
 // For a page with lo[d] <= k[d] <= hi[d], q.k <= sum over d of
-// max(q[d] lo[d], q[d] hi[d]) = sum of max(q,0) hi + min(q,0) lo: a product
-// of the vector (q+, q-) with (hi, lo), twice head_dim long.  Neighbouring
+// max(q[d] lo[d], q[d] hi[d]), for finite bounds the sum of max(q,0) hi +
+// min(q,0) lo: a product of the vector (q+, q-) with (hi, lo), twice head_dim
+// long.  (With infinite bounds the product has 0 times infinity where the
+// maximum has none; such pages are left to the sums in 64 bits.)  Neighbouring
 // scores decide which pages are read, so the definition sums in 64 bits and
 // rounds once; the kernels get there in two steps:
 //   1. k_scores multiplies on the matrix cores in 32 bits, and a second
@@ -161,6 +163,9 @@ constexpr uint32_t kWaveBlocks = 64;
 // absolute values: 2 * dim additions, each off by at most 2^-23 (which covers
 // rounding towards zero inside the matrix cores); the products are exact.
 __host__ __device__ constexpr float sum_error(int dim) { return (float)dim / 4194304.0f; }
+
+// Sums of absolute values from here on may overflow in another order.
+constexpr float kLargestSum = 1e38f;
 
 // Blocks of row r (0 where its sequence or length is not valid).
 __device__ __forceinline__ uint32_t row_blocks(const SelectArgs& a, uint64_t r, int64_t* seq) {
@@ -331,9 +336,10 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
                             // a NaN is left out: fmaxf takes its other argument
                             v[i] = (heads[c] >> i) & 1u ? fmaxf(s[i], -__builtin_inff()) : -__builtin_inff();
                             w[i] = wp[i] - wm[i];
-                            // (a NaN is a NaN in 64 bits too; an infinite sum may be
-                            // an overflow of 32 bits and makes every page near)
-                            w[i] = fmaxf(w[i], 0.f);
+                            // infinite or NaN (an infinite bound, a NaN in q or the
+                            // bounds, an overflow of 32 bits or nearly one): nothing
+                            // is known of the score, and every page is near
+                            w[i] = w[i] < kLargestSum ? fmaxf(w[i], 0.f) : __builtin_inff();
                         }
                         if constexpr (ONE_ROW) {
                             float m = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
@@ -592,9 +598,10 @@ __device__ __forceinline__ uint32_t exact_key(const SelectArgs& a, uint64_t r, u
                 for (int e = 0; e < 8; ++e) {
                     const int sh = 16 * (e & 1);
                     const double y = (double)E::from_bits(x[e >> 1] >> sh);
-                    // (a NaN stays in both halves)
-                    s += (y < 0.0 ? 0.0 : y) * (double)E::from_bits(hi[e >> 1] >> sh) +
-                         (y > 0.0 ? 0.0 : y) * (double)E::from_bits(lo[e >> 1] >> sh);
+                    const double to_lo = y * (double)E::from_bits(lo[e >> 1] >> sh);
+                    const double to_hi = y * (double)E::from_bits(hi[e >> 1] >> sh);
+                    // the larger, or a NaN of either
+                    s += to_lo != to_lo || to_lo > to_hi ? to_lo : to_hi;
                 }
             }
         }
@@ -695,8 +702,7 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
             // largest true one lies between t_lo and t_hi widened by slack;
             // pages that are further than two of them outside are decided
             // (a third covers the roundings of these bounds and of the score).
-            // An infinite slack (the products overflow 32 bits, or bounds are
-            // infinite) decides none.
+            // An infinite slack (kLargestSum) decides none.
             const bool bounded = slack < __builtin_inff();
             const uint32_t near_lo = order_of(bounded ? t_lo - 3.f * slack : -__builtin_inff());
             const uint32_t near_hi = order_of(bounded ? t_hi + 3.f * slack : __builtin_inff());
@@ -774,7 +780,7 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
                 }
             }
         } else {
-            // no slack (all products zero, or NaN): the sums as they are
+            // no slack (all products zero): the sums as they are
             cut = nth_largest(want, lo, hi, sh, turn, &above, own_keys);
             ties = want - above;
         }
