@@ -260,8 +260,8 @@ ibp_status ibp_gather_decompress_split(ibp_meta_t meta, const void* slots, uint6
 /* ---------------------------------------------------------------------------
  * Pages of a key/value cache.  A pool is fixed slots with their bitmask, as
  * ibp_compress leaves them: a closed page may be a record (bit 1), the page
- * that is still being filled is a raw slot (bit 0) that the caller writes in
- * place.  A block table (device int64, row-major) holds the slot ids of a
+ * that is still being filled is a raw slot (bit 0, see ibp_pages_alloc_raw)
+ * that the caller writes in place.  A block table (device int64, row-major) holds the slot ids of a
  * sequence's pages in order, -1 where there is none; refs (device int32, one
  * per slot) counts who holds a page, 0 = free.
  *
@@ -286,15 +286,22 @@ ibp_status ibp_pages_copy(ibp_meta_t meta, const void* src_slots, uint64_t n_src
                           const int64_t* src_ids, void* dst_slots, uint64_t n_dst, uint32_t* dst_bitmask,
                           const int64_t* dst_ids, uint64_t n, hipStream_t stream);
 
-/* Workspace bytes of the next calls: n = 0 for ibp_pages_alloc and
- * ibp_pages_compact, forks * heads for ibp_pages_fork. */
+/* Workspace bytes of the next calls: n = 0 for ibp_pages_alloc,
+ * ibp_pages_alloc_raw and ibp_pages_compact, forks * heads for
+ * ibp_pages_fork. */
 uint64_t ibp_pages_workspace(uint64_t n_slots, uint64_t n);
 
 /* ids[0..n) <- the n lowest free slots in ascending order, whose counts
  * become 1.  With fewer free slots the rest of ids is -1 and IBP_ERR_NOMEM
- * is latched. */
+ * is latched.  The slots' bitmask bits stay as they were, 1 where a record was
+ * freed: for slots that ibp_pages_copy or an encode will fill. */
 ibp_status ibp_pages_alloc(ibp_meta_t meta, int32_t* refs, uint64_t n_slots, int64_t* ids, uint64_t n,
                            void* workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+/* The same for pages that the caller writes in place: the bits of the slots
+ * handed out become 0 (raw). */
+ibp_status ibp_pages_alloc_raw(ibp_meta_t meta, int32_t* refs, uint64_t n_slots, uint32_t* bitmask, int64_t* ids,
+                               uint64_t n, void* workspace, uint64_t workspace_bytes, hipStream_t stream);
 
 /* Sequence children[i] becomes a fork of sequence parents[i] (device int64,
  * rows of table: n_seqs x n_heads x table_blocks ids): the lens[parent] /

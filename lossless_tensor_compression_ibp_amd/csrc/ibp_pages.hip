@@ -232,12 +232,14 @@ __device__ __forceinline__ uint64_t free_before(const int32_t* refs, uint64_t n_
     return r;
 }
 
-// ids[r] <- the r-th free slot, r < n.  TAKE: the slots' counts become 1, ids
-// without a slot -1, and too few free slots latch kErrFull.
+// ids[r] <- the r-th free slot, r < n.  TAKE: the slots' counts become 1 (and
+// their bits in bitmask, if given, 0), ids without a slot -1, and too few free
+// slots latch kErrFull.
 template <bool TAKE, bool SCAN>
 __global__ __launch_bounds__(SCAN ? kListBlock : kCountBlock) void k_list_free(int32_t* refs, uint64_t n_slots,
                                                                               const uint32_t* counts, int64_t* ids,
-                                                                              uint64_t n, uint32_t* err) {
+                                                                              uint64_t n, uint32_t* bitmask,
+                                                                              uint32_t* err) {
     static_assert(!(TAKE && SCAN), "other workgroups would read counts while this one writes its own");
     const uint64_t base = ((uint64_t)blockIdx.x * blockDim.x + threadIdx.x) * kCountPer;
     uint32_t f = free_flags(refs, n_slots, base);
@@ -247,7 +249,10 @@ __global__ __launch_bounds__(SCAN ? kListBlock : kCountBlock) void k_list_free(i
         const uint64_t slot = base + (uint32_t)__builtin_ctz(f);
         f &= f - 1;
         ids[r++] = (int64_t)slot;
-        if (TAKE) refs[slot] = 1;
+        if (TAKE) {
+            refs[slot] = 1;
+            if (bitmask) set_bit(bitmask, slot, 0);
+        }
     }
     if (blockIdx.x == gridDim.x - 1 && all < n) {
         for (uint64_t i = all + threadIdx.x; i < n; i += blockDim.x) ids[i] = -1;
@@ -505,21 +510,38 @@ static ibp_status check_workspace(ibp_meta_t h, const void* ws, uint64_t bytes, 
     return IBP_OK;
 }
 
+// bitmask: NULL, or where the bits of the slots taken become 0.
+static ibp_status take_slots(ibp_meta_t h, int32_t* refs, uint64_t n_slots, uint32_t* bitmask, int64_t* ids, uint64_t n,
+                             void* workspace, uint64_t workspace_bytes, hipStream_t stream) {
+    if (n_slots == 0 || n_slots > kMaxPoolSlots || n > kMaxPoolSlots) return IBP_ERR_INVALID_ARG;
+    if (!device_only(refs, h->device) || !device_only(ids, h->device)) return IBP_ERR_INVALID_ARG;
+    if (bitmask && !device_only(bitmask, h->device)) return IBP_ERR_INVALID_ARG;
+    ibp_status st = check_workspace(h, workspace, workspace_bytes, ibp_pages_workspace(n_slots, 0));
+    if (st != IBP_OK) return st;
+    uint32_t* counts = static_cast<uint32_t*>(workspace);
+    IBP_TRY(launch_count_free(refs, n_slots, counts, stream));
+    hipLaunchKernelGGL((k_list_free<true, false>), dim3((uint32_t)count_blocks(n_slots)), dim3(kCountBlock), 0, stream, refs,
+                       n_slots, counts, ids, n, bitmask, h->d_err);
+    return from_hip(hipGetLastError());
+}
+
 ibp_status ibp_pages_alloc(ibp_meta_t h, int32_t* refs, uint64_t n_slots, int64_t* ids, uint64_t n, void* workspace,
                            uint64_t workspace_bytes, hipStream_t stream) {
     if (!h) return IBP_ERR_INVALID_ARG;
     if (n == 0) return IBP_OK;
     DeviceGuard guard(h->device);
     if (!guard.ok) return IBP_ERR_DEVICE;
-    if (n_slots == 0 || n_slots > kMaxPoolSlots || n > kMaxPoolSlots) return IBP_ERR_INVALID_ARG;
-    if (!device_only(refs, h->device) || !device_only(ids, h->device)) return IBP_ERR_INVALID_ARG;
-    ibp_status st = check_workspace(h, workspace, workspace_bytes, ibp_pages_workspace(n_slots, 0));
-    if (st != IBP_OK) return st;
-    uint32_t* counts = static_cast<uint32_t*>(workspace);
-    IBP_TRY(launch_count_free(refs, n_slots, counts, stream));
-    hipLaunchKernelGGL((k_list_free<true, false>), dim3((uint32_t)count_blocks(n_slots)), dim3(kCountBlock), 0, stream, refs,
-                       n_slots, counts, ids, n, h->d_err);
-    return from_hip(hipGetLastError());
+    return take_slots(h, refs, n_slots, nullptr, ids, n, workspace, workspace_bytes, stream);
+}
+
+ibp_status ibp_pages_alloc_raw(ibp_meta_t h, int32_t* refs, uint64_t n_slots, uint32_t* bitmask, int64_t* ids,
+                               uint64_t n, void* workspace, uint64_t workspace_bytes, hipStream_t stream) {
+    if (!h) return IBP_ERR_INVALID_ARG;
+    if (n == 0) return IBP_OK;
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return IBP_ERR_DEVICE;
+    if (!bitmask) return IBP_ERR_INVALID_ARG;
+    return take_slots(h, refs, n_slots, bitmask, ids, n, workspace, workspace_bytes, stream);
 }
 
 ibp_status ibp_pages_fork(ibp_meta_t h, void* slots, uint64_t n_slots, uint32_t* bitmask, int32_t* refs,
@@ -545,11 +567,11 @@ ibp_status ibp_pages_fork(ibp_meta_t h, void* slots, uint64_t n_slots, uint32_t*
     int64_t* fresh = static_cast<int64_t*>(workspace) + count_words(n_slots);
     if (n_slots <= kListSlots) {
         hipLaunchKernelGGL((k_list_free<false, true>), scan_grid(n_slots), dim3(kListBlock), 0, stream, refs, n_slots,
-                           nullptr, fresh, n * n_heads, h->d_err);
+                           nullptr, fresh, n * n_heads, nullptr, h->d_err);
     } else {
         IBP_TRY(launch_count_free(refs, n_slots, counts, stream));
         hipLaunchKernelGGL((k_list_free<false, false>), dim3((uint32_t)count_blocks(n_slots)), dim3(kCountBlock), 0,
-                           stream, refs, n_slots, counts, fresh, n * n_heads, h->d_err);
+                           stream, refs, n_slots, counts, fresh, n * n_heads, nullptr, h->d_err);
     }
     IBP_TRY(hipGetLastError());
     const Geo geo = make_geo(h, true, kLongTileWordsDecode);

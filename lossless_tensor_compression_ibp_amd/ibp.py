@@ -37,7 +37,7 @@ ABI_FUNCTIONS = (
     "ibp_packed_offsets", "ibp_compress_packed", "ibp_decompress_packed", "ibp_gather_decompress_packed",
     "ibp_compress_split", "ibp_decompress_split", "ibp_gather_decompress_split",
     "ibp_decompress_noalloc",
-    "ibp_pages_copy", "ibp_pages_workspace", "ibp_pages_alloc", "ibp_pages_fork", "ibp_pages_free",
+    "ibp_pages_copy", "ibp_pages_workspace", "ibp_pages_alloc", "ibp_pages_alloc_raw", "ibp_pages_fork", "ibp_pages_free",
     "ibp_pages_compact", "ibp_tree_attention_workspace", "ibp_tree_attention", "ibp_page_bounds",
     "ibp_select_pages_workspace", "ibp_select_pages", "ibp_sparse_attention_workspace", "ibp_sparse_attention",
 )
@@ -108,6 +108,7 @@ def lib():
         L.ibp_pages_copy.argtypes = [p, p, u64, p, p, p, u64, p, p, u64, p]
         L.ibp_pages_workspace.argtypes = [u64, u64]
         L.ibp_pages_alloc.argtypes = [p, p, u64, p, u64, p, u64, p]
+        L.ibp_pages_alloc_raw.argtypes = [p, p, u64, p, p, u64, p, u64, p]
         L.ibp_pages_fork.argtypes = [p, p, u64, p, p, p, u64, u32, u64, p, u32, p, p, u64, p, u64, p]
         L.ibp_pages_free.argtypes = [p, p, u64, p, u64, u32, u64, p, u64, p]
         L.ibp_pages_compact.argtypes = [p, p, u64, p, p, p, p, p, u64, p, u64, p]
@@ -512,12 +513,25 @@ def ibp_pages_workspace(n_slots: int, n: int = 0) -> int:
 
 
 def ibp_pages_alloc(meta: Meta, refs: torch.Tensor, n_slots: int, ids: torch.Tensor, workspace=None, stream=None):
-    """ids <- the lowest free slots, in order; their counts become 1."""
+    """ids <- the lowest free slots, in order; their counts become 1.  Their
+    bitmask bits stay: see ibp_pages_alloc_raw."""
     _typed(refs, torch.int32, "refs", int(n_slots))
     _typed(ids, torch.int64, "ids")
     ws = _workspace(workspace, ibp_pages_workspace(n_slots), refs, stream)
     _check(lib().ibp_pages_alloc(meta, _flat(refs), int(n_slots), _flat(ids), ids.numel(), _flat(ws), _bytes_of(ws),
                                  _stream_of(stream, refs)), "ibp_pages_alloc")
+
+
+def ibp_pages_alloc_raw(meta: Meta, refs: torch.Tensor, n_slots: int, bitmask: torch.Tensor, ids: torch.Tensor,
+                        workspace=None, stream=None):
+    """The same for pages that are written in place: the slots' bits in bitmask
+    become 0 (raw)."""
+    _typed(refs, torch.int32, "refs", int(n_slots))
+    _typed(ids, torch.int64, "ids")
+    _need(bitmask, _bitmask_bytes(n_slots), "bitmask")
+    ws = _workspace(workspace, ibp_pages_workspace(n_slots), refs, stream)
+    _check(lib().ibp_pages_alloc_raw(meta, _flat(refs), int(n_slots), _flat(bitmask), _flat(ids), ids.numel(), _flat(ws),
+                                     _bytes_of(ws), _stream_of(stream, refs)), "ibp_pages_alloc_raw")
 
 
 def _table_shape(table: torch.Tensor):
