@@ -271,7 +271,8 @@ ibp_status ibp_gather_decompress_split(ibp_meta_t meta, const void* slots, uint6
  * or reads results on the host, so every one may be captured in a HIP graph;
  * scratch comes from the caller (`workspace`, device, 16-byte aligned), and
  * two calls that may overlap in time must not share it.  Ids that are neither
- * -1 nor a slot latch IBP_ERR_RANGE.
+ * -1 nor a slot latch IBP_ERR_RANGE.  A call forks at most 2^24 - 1 rows of
+ * the table (forks times heads); more return IBP_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------- */
 
 /* The item of slot src_ids[i] (its record, or the whole raw page) and its
@@ -351,6 +352,10 @@ ibp_status ibp_pages_compact(ibp_meta_t meta, void* slots, uint64_t n_slots, uin
  * only keys whose score is -infinity, gives zeros and lse -infinity.  What
  * lies in a page behind a sequence's last token, and keys and values that a
  * row does not see, never reach its result, infinities and NaN included.
+ *
+ * A call is one launch of at most 2^24 - 1 workgroups, one or more for each
+ * (row, or sequence of drafted tokens; key/value head); larger ones return
+ * IBP_ERR_UNSUPPORTED before anything is queued and are given in parts.
  * ------------------------------------------------------------------------- */
 typedef enum ibp_dtype { IBP_BF16 = 0, IBP_FP16 = 1 } ibp_dtype;
 
@@ -417,7 +422,11 @@ ibp_status ibp_page_bounds(const ibp_pages* k, uint32_t dtype, uint32_t head_dim
  * and rounded to 32; equal scores go to the lower block, and a NaN counts as
  * the lowest (an infinite bound is one like any other: only 0 times infinity
  * and sums of both infinities are NaN).  bounds: pool-wide, as ibp_page_bounds leaves them, indexed by
- * the ids of the keys' table.  At most 2^17 blocks per row.  Of a, max_len,
+ * the ids of the keys' table.  At most 2^17 blocks per row and 2^22 - 1 rows
+ * times key/value heads.  Rows four times as many as the sequences, in groups
+ * of up to 16 query heads: at most 262,140; others in tables of more than 1,024
+ * blocks: 65,535.  More may return IBP_ERR_UNSUPPORTED, before anything is
+ * queued, and are given in parts.  Of a, max_len,
  * max_new, scale and the new_ strides are not read. */
 uint64_t ibp_select_pages_workspace(const ibp_attention* a);
 ibp_status ibp_select_pages(ibp_meta_t meta, const ibp_attention* a, const void* q, const void* bounds,

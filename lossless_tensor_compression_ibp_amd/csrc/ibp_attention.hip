@@ -89,7 +89,8 @@ ibp_status fill_args(const ibp_pages* k, const ibp_pages* v, const ibp_attention
             return IBP_ERR_INVALID_ARG;
     }
     const uint64_t groups = items * a->n_kv_heads * p.row_tiles * p.splits;
-    if (groups > 0x7FFFFFFFull || a->n_rows * a->n_q_heads * (a->head_dim / 4) / 256 > 0x7FFFFFFEull)
+    if (groups > max_workgroups(kWave * std::max(kFewWaves, kManyWaves)) ||
+        (p.splits > 1 && a->n_rows * a->n_q_heads * (a->head_dim / 4) > kMaxLaunchThreads - 255))
         return IBP_ERR_UNSUPPORTED;
     x->q = static_cast<const uint16_t*>(q);
     x->k_table = k_table;

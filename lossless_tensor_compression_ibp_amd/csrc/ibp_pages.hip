@@ -143,15 +143,16 @@ __global__ __launch_bounds__(kWave * kPageWaves) void k_pages_copy(Tables t, Geo
                                                                    uint8_t* dst, uint64_t n_dst, uint32_t* dst_bm,
                                                                    const int64_t* dst_ids, uint64_t n,
                                                                    uint32_t* err) {
-    const uint64_t i = (uint64_t)blockIdx.x * kPageWaves + uniform(threadIdx.x / kWave);
-    if (i >= n) return;
-    const int64_t a = (int64_t)uniform64((uint64_t)src_ids[i]), b = (int64_t)uniform64((uint64_t)dst_ids[i]);
-    if (a == -1 || b == -1) return;
-    if (a < 0 || (uint64_t)a >= n_src || b < 0 || (uint64_t)b >= n_dst) {
-        latch_error(err, kErrRange);
-        return;
+    const uint64_t stride = (uint64_t)gridDim.x * kPageWaves;
+    for (uint64_t i = (uint64_t)blockIdx.x * kPageWaves + uniform(threadIdx.x / kWave); i < n; i += stride) {
+        const int64_t a = (int64_t)uniform64((uint64_t)src_ids[i]), b = (int64_t)uniform64((uint64_t)dst_ids[i]);
+        if (a == -1 || b == -1) continue;
+        if (a < 0 || (uint64_t)a >= n_src || b < 0 || (uint64_t)b >= n_dst) {
+            latch_error(err, kErrRange);
+            continue;
+        }
+        copy_item<NV>(t, g, src, src_bm, (uint64_t)a, dst, dst_bm, (uint64_t)b, err);
     }
-    copy_item<NV>(t, g, src, src_bm, (uint64_t)a, dst, dst_bm, (uint64_t)b, err);
 }
 
 // ---------------------------------------------------------------------------
@@ -340,27 +341,28 @@ __global__ __launch_bounds__(256) void k_pages_fork(Tables t, Geo g, ForkArgs a,
     }
 }
 
-// One thread per table entry of the sequences given: the entry becomes -1 and
+// A table entry of the sequences given after another: the entry becomes -1 and
 // its page's count falls by one.  The exchange makes a sequence that is given
 // twice count once.
 __global__ __launch_bounds__(256) void k_pages_free(int32_t* refs, uint64_t n_slots, int64_t* table, uint64_t n_seqs,
                                                     uint64_t row, const int64_t* seqs, uint64_t n, uint32_t* err) {
-    const uint64_t e = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (e >= n * row) return;
-    const int64_t s = seqs[e / row];
-    bool range = s < 0 || (uint64_t)s >= n_seqs, below = false;
-    if (!range) {
+    const uint64_t stride = (uint64_t)gridDim.x * blockDim.x;
+    bool range = false, below = false;
+    for (uint64_t e = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n * row; e += stride) {
+        const int64_t s = seqs[e / row];
+        if (s < 0 || (uint64_t)s >= n_seqs) {
+            range = true;
+            continue;
+        }
         unsigned long long* p = reinterpret_cast<unsigned long long*>(table + (uint64_t)s * row + e % row);
         const int64_t id = (int64_t)atomicExch(p, ~0ull);
-        if (id >= 0) {
-            if ((uint64_t)id >= n_slots) {
-                range = true;
-            } else if (atomicSub(refs + id, 1) <= 0) {
+        if (id >= 0 && (uint64_t)id < n_slots) {
+            if (atomicSub(refs + id, 1) <= 0) {
                 atomicAdd(refs + id, 1);
                 below = true;
             }
-        } else {
-            range = id != -1;
+        } else if (id != -1) {
+            range = true;
         }
     }
     if (range) atomicCAS(err, 0u, (uint32_t)kErrRange);
@@ -423,14 +425,22 @@ __global__ __launch_bounds__(kWave * kPageWaves) void k_compact_move(Tables t, G
 
 __global__ __launch_bounds__(256) void k_remap(const int64_t* map, uint64_t n_slots, int64_t* table, uint64_t n,
                                                uint32_t* err) {
-    const uint64_t e = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (e >= n) return;
-    const int64_t id = table[e];
-    if (id == -1) return;
-    if (id >= 0 && (uint64_t)id < n_slots)
-        table[e] = map[id];
-    else
-        atomicCAS(err, 0u, (uint32_t)kErrRange);
+    const uint64_t stride = (uint64_t)gridDim.x * blockDim.x;
+    for (uint64_t e = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += stride) {
+        const int64_t id = table[e];
+        if (id == -1) continue;
+        if (id >= 0 && (uint64_t)id < n_slots)
+            table[e] = map[id];
+        else
+            atomicCAS(err, 0u, (uint32_t)kErrRange);
+    }
+}
+
+// Workgroups of the kernels that stride over their items: one per `per` of
+// them, and fewer only where one launch does not hold as many.
+constexpr uint64_t kMaxStriding = 1u << 22;
+static dim3 striding_grid(uint64_t items, uint64_t per) {
+    return dim3((uint32_t)std::min<uint64_t>((items + per - 1) / per, kMaxStriding));
 }
 
 // f.template operator()<NV>() for the vectors per lane that a page of L bytes takes.
@@ -492,7 +502,7 @@ ibp_status ibp_pages_copy(ibp_meta_t h, const void* src_slots, uint64_t n_src, c
     if (st != IBP_OK) return st;
     const Geo geo = make_geo(h, true, kLongTileWordsDecode);
     return from_hip(by_vectors(L, [&](auto nv) {
-        hipLaunchKernelGGL((k_pages_copy<decltype(nv)::value>), dim3((uint32_t)((n + kPageWaves - 1) / kPageWaves)),
+        hipLaunchKernelGGL((k_pages_copy<decltype(nv)::value>), striding_grid(n, kPageWaves),
                            dim3(kWave * kPageWaves), 0, stream, h->tabs, geo, static_cast<const uint8_t*>(src_slots),
                            n_src, src_bitmask, src_ids, static_cast<uint8_t*>(dst_slots), n_dst, dst_bitmask, dst_ids,
                            n, h->d_err);
@@ -553,8 +563,9 @@ ibp_status ibp_pages_fork(ibp_meta_t h, void* slots, uint64_t n_slots, uint32_t*
     DeviceGuard guard(h->device);
     if (!guard.ok) return IBP_ERR_DEVICE;
     if (n_slots == 0 || n_slots > kMaxPoolSlots || n_heads == 0 || page_tokens == 0 || table_blocks == 0 ||
-        table_blocks > (1ull << 31) / page_tokens || n_seqs > kMaxPoolSlots || n > 0x7FFFFFFFull / n_heads)
+        table_blocks > (1ull << 31) / page_tokens || n_seqs > kMaxPoolSlots)
         return IBP_ERR_INVALID_ARG;
+    if (n > max_workgroups(256) / n_heads) return IBP_ERR_UNSUPPORTED;
     if (!device_or_pinned(slots, h->device)) return IBP_ERR_INVALID_ARG;
     for (const void* p : {(const void*)bitmask, (const void*)refs, (const void*)table, (const void*)lens,
                           (const void*)parents, (const void*)children})
@@ -594,10 +605,10 @@ ibp_status ibp_pages_free(ibp_meta_t h, int32_t* refs, uint64_t n_slots, int64_t
     if (n_slots == 0 || n_slots > kMaxPoolSlots || n_heads == 0 || table_blocks == 0 || table_blocks > (1ull << 31))
         return IBP_ERR_INVALID_ARG;
     const uint64_t row = n_heads * table_blocks;
-    if (n > (0x7FFFFFFFull * 256) / row) return IBP_ERR_INVALID_ARG;
+    if (n > (1ull << 62) / row) return IBP_ERR_INVALID_ARG;
     for (const void* p : {(const void*)refs, (const void*)table, (const void*)seqs})
         if (!device_only(p, h->device)) return IBP_ERR_INVALID_ARG;
-    hipLaunchKernelGGL(k_pages_free, dim3((uint32_t)((n * row + 255) / 256)), dim3(256), 0, stream, refs, n_slots,
+    hipLaunchKernelGGL(k_pages_free, striding_grid(n * row, 256), dim3(256), 0, stream, refs, n_slots,
                        table, n_seqs, row, seqs, n, h->d_err);
     return from_hip(hipGetLastError());
 }
@@ -609,7 +620,7 @@ ibp_status ibp_pages_compact(ibp_meta_t h, void* slots, uint64_t n_slots, uint32
     if (n_slots == 0) return IBP_OK;
     DeviceGuard guard(h->device);
     if (!guard.ok) return IBP_ERR_DEVICE;
-    if (n_slots > kMaxPoolSlots || n_entries > 0x7FFFFFFFull * 256) return IBP_ERR_INVALID_ARG;
+    if (n_slots > kMaxPoolSlots || n_entries > 1ull << 62) return IBP_ERR_INVALID_ARG;
     if (!device_or_pinned(slots, h->device)) return IBP_ERR_INVALID_ARG;
     for (const void* p : {(const void*)bitmask, (const void*)refs, (const void*)map, (const void*)n_live})
         if (!device_only(p, h->device)) return IBP_ERR_INVALID_ARG;
@@ -642,7 +653,7 @@ ibp_status ibp_pages_compact(ibp_meta_t h, void* slots, uint64_t n_slots, uint32
         return hipGetLastError();
     }));
     if (n_entries) {
-        hipLaunchKernelGGL(k_remap, dim3((uint32_t)((n_entries + 255) / 256)), dim3(256), 0, stream, map, n_slots,
+        hipLaunchKernelGGL(k_remap, striding_grid(n_entries, 256), dim3(256), 0, stream, map, n_slots,
                            table, n_entries, h->d_err);
         IBP_TRY(hipGetLastError());
     }

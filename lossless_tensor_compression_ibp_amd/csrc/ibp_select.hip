@@ -975,16 +975,23 @@ ibp_status ibp_select_pages(ibp_meta_t h, const ibp_attention* a, const void* q,
     s.span = shared ? (uint32_t)std::min<uint64_t>(std::max<uint64_t>(1, (all_chunks + 767) / 768), 64) : 1;
     const uint64_t per_wg_rows = (uint64_t)s.wave_rows * (shared ? kScoreWaves : 1);
     const uint64_t groups = (a->n_rows + per_wg_rows - 1) / per_wg_rows;
-    if (groups > 65535 || a->n_kv_heads > 65535 || a->n_rows * a->n_kv_heads > 0x7FFFFFFFull)
-        return IBP_ERR_UNSUPPORTED;
     const bool scored = a->table_blocks > n_blocks && n_blocks > keep_first + keep_last;
+    const bool one_launch = scored && !shared && a->table_blocks <= kOneLaunchBlocks;
+    const bool keys = a->table_blocks <= kLdsKeys;
+    // waves that choose: eight blocks per thread
+    const uint32_t waves =
+        one_launch ? kSelectWaves
+        : keys     ? (uint32_t)std::min<uint64_t>(kMaxChooseWaves, std::max<uint64_t>(4, (a->table_blocks + 8 * kWave - 1) / (8 * kWave)))
+                   : kMaxChooseWaves;
+    if (a->n_rows * a->n_kv_heads > max_workgroups(kWave * waves) || (scored && !one_launch && groups > 65535))
+        return IBP_ERR_UNSUPPORTED;
     auto launch = [&](auto e, auto dc) {
         using E = decltype(e);
         constexpr int D = decltype(dc)::value;
         const dim3 grid((uint32_t)(a->n_rows * a->n_kv_heads));
         const uint32_t marks = (uint32_t)(4 * ((a->table_blocks + 31) / 32));
-        if (scored && !shared && a->table_blocks <= kOneLaunchBlocks) {
-            hipLaunchKernelGGL((k_select<E, D>), grid, dim3(kWave * kSelectWaves),
+        if (one_launch) {
+            hipLaunchKernelGGL((k_select<E, D>), grid, dim3(kWave * waves),
                                marks + (uint32_t)(4 * a->table_blocks), stream, s);
             return hipGetLastError();
         }
@@ -1005,15 +1012,11 @@ ibp_status ibp_select_pages(ibp_meta_t h, const ibp_attention* a, const void* q,
             const hipError_t err = hipGetLastError();
             if (err != hipSuccess) return err;
         }
-        if (a->table_blocks <= kLdsKeys) {
-            // eight blocks per thread
-            const uint32_t waves =
-                (uint32_t)std::min<uint64_t>(16, std::max<uint64_t>(4, (a->table_blocks + 8 * kWave - 1) / (8 * kWave)));
+        if (keys)
             hipLaunchKernelGGL((k_choose<E, D, true>), grid, dim3(kWave * waves),
                                marks + (uint32_t)(4 * a->table_blocks), stream, s);
-        } else {
-            hipLaunchKernelGGL((k_choose<E, D, false>), grid, dim3(1024), marks, stream, s);
-        }
+        else
+            hipLaunchKernelGGL((k_choose<E, D, false>), grid, dim3(kWave * waves), marks, stream, s);
         return hipGetLastError();
     };
     auto by_dim = [&](auto e) {
