@@ -331,10 +331,23 @@ struct Rows {
         for (int e = 0; e < 4; ++e) s[t][u][e] = (seen >> (4 * g + e)) & 1u ? s[t][u][e] : -__builtin_inff();
     }
 
-    // The running maximum.  It is moved only when a score passes it by more
-    // than 8 (weights then stay below 2^8 and sums far from overflow), so most
-    // steps rescale nothing; one branch for all rows leaves the rest of a step
-    // in one block, where the compiler can run weights beside products.
+    // The running maximum, less E::kLead, is the exponent m that weights are
+    // taken against: exp2(score - m).  It is moved only when a score passes it
+    // by more than kLead + 8 (weights then stay below 2^(kLead + 8) and sums
+    // far from overflow), so most steps rescale nothing; one branch for all
+    // rows leaves the rest of a step in one block, where the compiler can run
+    // weights beside products.
+    //
+    // The weights are rounded to the data's type, once, for the matrix product
+    // with the values; their sum l takes them unrounded, in 32 bits.  (The
+    // matrix cores do a sixteenth of the products in 32 bits, and weights split
+    // in two 16-bit parts would take twice as many.)  Each is off by half a
+    // step at most, 2^-8 or 2^-11 of its value, which moves a row by that share
+    // of its mean |v| at most.  bf16 has the range of 32 bits.  In fp16 numbers
+    // below 2^-14 have steps of 2^-24, so with a largest weight of 1 a key 25
+    // octaves below it would weigh nothing here but count in l, and a long
+    // context of such keys is not nothing (65,535 of them: 0.2 %).  With 2^7
+    // to 2^15 for the largest weight a key loses at most 2^-32 of it.
     __device__ __forceinline__ void raise(float scale2) {
         float top[MR];
         bool move = false;
@@ -348,12 +361,12 @@ struct Rows {
 #pragma unroll
             for (int u = 1; u < TILES; ++u) top[t] = fmaxf(top[t], x[u]);
             top[t] = max_over_four(top[t]) * scale2;
-            move = move || top[t] > m[t] + 8.f || (m[t] == -__builtin_inff() && top[t] != -__builtin_inff());
+            move = move || top[t] - m[t] > E::kLead + 8.f;  // (also the first one, from -infinity)
         }
         if (ballot(move)) {
 #pragma unroll
             for (int t = 0; t < MR; ++t) {
-                const float m_new = fmaxf(m[t], top[t]);
+                const float m_new = fmaxf(m[t], top[t] - E::kLead);
                 const float f = m_new == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(m[t] - m_new);
                 m[t] = m_new;
                 l[t] *= f;

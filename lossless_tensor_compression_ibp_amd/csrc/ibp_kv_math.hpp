@@ -36,6 +36,8 @@ struct Bf16 {
     }
     // all exponent bits set in either half: an infinity or a NaN
     static constexpr uint32_t kExponent = 0x7F80u;
+    // octaves above 1 at which the largest softmax weight is kept (see raise)
+    static constexpr float kLead = 0.f;
 };
 
 struct Fp16 {
@@ -51,6 +53,7 @@ struct Fp16 {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
     static constexpr uint32_t kExponent = 0x7C00u;
+    static constexpr float kLead = 7.f;
 };
 
 // Eight numbers of a dense row, which need not start on more than two bytes
