@@ -331,12 +331,16 @@ struct Rows {
         for (int e = 0; e < 4; ++e) s[t][u][e] = (seen >> (4 * g + e)) & 1u ? s[t][u][e] : -__builtin_inff();
     }
 
-    // The running maximum, less E::kLead, is the exponent m that weights are
-    // taken against: exp2(score - m).  It is moved only when a score passes it
-    // by more than kLead + 8 (weights then stay below 2^(kLead + 8) and sums
-    // far from overflow), so most steps rescale nothing; one branch for all
-    // rows leaves the rest of a step in one block, where the compiler can run
-    // weights beside products.
+    // Scores in octaves, and their running maximum.  The maximum, less
+    // E::kLead, is the exponent m that weights are taken against:
+    // exp2(score - m).  It is moved only when a score passes it by more than
+    // kLead + 8 (weights then stay below 2^(kLead + 8) and sums far from
+    // overflow), so most steps rescale nothing; one branch for all rows leaves
+    // the rest of a step in one block, where the compiler can run weights
+    // beside products.  Scores are scaled and rounded here, before the maximum
+    // is taken off: with both in one multiply-add the highest score would
+    // differ from the maximum by up to half a step of 32 bits, which past 2^31
+    // octaves is more than a weight can hold.
     //
     // The weights are rounded to the data's type, once, for the matrix product
     // with the values; their sum l takes them unrounded, in 32 bits.  (The
@@ -355,12 +359,14 @@ struct Rows {
         for (int t = 0; t < MR; ++t) {
             float x[TILES];
 #pragma unroll
-            for (int u = 0; u < TILES; ++u)
+            for (int u = 0; u < TILES; ++u) {
+                s[t][u] *= scale2;
                 x[u] = fmaxf(fmaxf(s[t][u][0], s[t][u][1]), fmaxf(s[t][u][2], s[t][u][3]));
+            }
             top[t] = x[0];
 #pragma unroll
             for (int u = 1; u < TILES; ++u) top[t] = fmaxf(top[t], x[u]);
-            top[t] = max_over_four(top[t]) * scale2;
+            top[t] = max_over_four(top[t]);
             move = move || top[t] - m[t] > E::kLead + 8.f;  // (also the first one, from -infinity)
         }
         if (ballot(move)) {
@@ -377,7 +383,8 @@ struct Rows {
     }
 
     // Weights, their sum, and O^T += V^T P^T, two tiles of tokens at a time.
-    __device__ __forceinline__ void values(const char* vals, int stride, float scale2) {
+    __device__ __forceinline__ void values(const char* vals, int stride) {
+#pragma clang fp contract(off)  // (scores stay rounded, see above)
         const uint32_t col = lane_id() & 15u, g = lane_id() >> 4;
         float base[MR];
 #pragma unroll
@@ -390,8 +397,7 @@ struct Rows {
 #pragma unroll
                 for (int v = u; v < u + 2; ++v) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        s[t][v][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][v][e], scale2, base[t]));
+                    for (int e = 0; e < 4; ++e) s[t][v][e] = __builtin_amdgcn_exp2f(s[t][v][e] + base[t]);
                     l[t] += (s[t][v][0] + s[t][v][1]) + (s[t][v][2] + s[t][v][3]);
                 }
                 const u32x4 x = {E::pack(s[t][u][0], s[t][u][1]), E::pack(s[t][u][2], s[t][u][3]),
@@ -684,7 +690,7 @@ __global__ __launch_bounds__(kWave * kFewWaves, 2) void k_attend_few(AttnArgs a)
                 load(st_b, i + 1, true, id_v);
             advance(i + 1);
         }
-        rows.values(tile, S::RV, a.scale2);
+        rows.values(tile, S::RV);
         lds_order();
         if (more) take_sees();
     }
@@ -863,7 +869,7 @@ __global__ __launch_bounds__(kWave * kManyWaves, 2) void k_attend_many(AttnArgs 
             }
         }
         rows.raise(a.scale2);
-        rows.values(area + STEP * S::RK, S::RV, a.scale2);
+        rows.values(area + STEP * S::RK, S::RV);
     }
 
     const ArgsPtr c = args_again();
