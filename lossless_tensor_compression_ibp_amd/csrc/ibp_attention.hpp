@@ -416,17 +416,27 @@ struct Rows {
     }
 };
 
+// Whether a row has any weight (or a NaN for one).  Without one it is zeros,
+// whatever the values are that weighed nothing.
+__device__ __forceinline__ bool has_weight(float l) { return l > 0.f || l != l; }
+
+// Four dims of a row whose weights are l: the quotient in the data's type.
+template <class E>
+__device__ __forceinline__ u32x2 row_of(f32x4 x, float l) {
+    const float inv = 1.f / l;
+    const u32x2 y = {E::pack(x[0] * inv, x[1] * inv), E::pack(x[2] * inv, x[3] * inv)};
+    return has_weight(l) ? y : u32x2{0u, 0u};
+}
+
 // Four dims of a row: the result, or this split's part of it.
 template <class E, int D>
 __device__ __forceinline__ void put_result(ArgsPtr c, uint32_t split, uint32_t row, uint32_t head, uint32_t d, f32x4 x,
                                            float m, float l) {
     const uint64_t rh = (uint64_t)row * (c->kv_heads * c->group) + head;
     if (c->splits == 1) {
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-        const u32x2 y = {E::pack(x[0] * inv, x[1] * inv), E::pack(x[2] * inv, x[3] * inv)};
-        *reinterpret_cast<u32x2*>(c->out + rh * D + d) = y;
+        *reinterpret_cast<u32x2*>(c->out + rh * D + d) = row_of<E>(x, l);
         if (d == 0 && c->lse)
-            c->lse[rh] = l > 0.f || l != l ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -__builtin_inff();
+            c->lse[rh] = has_weight(l) ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -__builtin_inff();
     } else {
         *reinterpret_cast<f32x4*>(c->part + (rh * c->splits + split) * D + d) = x;
         if (d == 0) {
@@ -439,15 +449,17 @@ __device__ __forceinline__ void put_result(ArgsPtr c, uint32_t split, uint32_t r
 // Whole workgroup, after its results are in memory: drafted values j_lo ..
 // j_hi - 1 that are infinite or NaN, added to the rows that see them.  (They
 // were taken out of the products, where they would have reached every row
-// through a weight of zero.)
+// through a weight of zero.)  weighed: of the workgroup's rows, those that have
+// a weight; of parts, k_join knows.
 template <class E, int D>
-__device__ __forceinline__ void add_odd_values(const AttnArgs& a, const Work& w, uint32_t rows_per_wg, uint32_t j_lo,
-                                               uint32_t j_hi) {
+__device__ __forceinline__ void add_odd_values(const AttnArgs& a, const Work& w, uint32_t rows_per_wg,
+                                               const bool* weighed, uint32_t j_lo, uint32_t j_hi) {
     const ArgsPtr c = args_again();
     const uint32_t n_rows = min(w.rows - w.rt * rows_per_wg, rows_per_wg);
 #pragma unroll 1
     for (uint32_t e = threadIdx.x; e < n_rows * D; e += blockDim.x) {
         const uint32_t d = e % D;
+        if (c->splits == 1 && !weighed[e / D]) continue;
         uint32_t head;
         const uint32_t row = row_of_group(a, w, w.rt * rows_per_wg + e / D, &head);
         float sum = 0.f;
@@ -499,6 +511,7 @@ __global__ __launch_bounds__(kWave * kFewWaves, 2) void k_attend_few(AttnArgs a)
     extern __shared__ __align__(16) uint32_t smem[];
     __shared__ float join_m[kFewWaves][16], join_l[kFewWaves][16];
     __shared__ uint32_t odd_values;  // an infinity or NaN among the drafted values
+    __shared__ bool weighed[kRowsWg];
     const uint32_t lane = lane_id(), wib = uniform(threadIdx.x / kWave);
     const uint32_t col = lane & 15u, g = lane >> 4;
 
@@ -729,13 +742,14 @@ __global__ __launch_bounds__(kWave * kFewWaves, 2) void k_attend_few(AttnArgs a)
             uint32_t head;
             const uint32_t row = row_of_group(a, w, rho, &head);
             put_result<E, D>(c, w.split, row, head, d, x, mm, ll);
+            if (TREE && d == 0) weighed[16 * t + r] = has_weight(ll);
         }
     }
     if constexpr (TREE) {
         if (ballot(odd) && lane == 0) odd_values = 1;
         __syncthreads();
         if (odd_values)
-            add_odd_values<E, D>(a, w, kRowsWg, s_lo > ctx_steps ? (s_lo - ctx_steps) * STEP : 0u,
+            add_odd_values<E, D>(a, w, kRowsWg, weighed, s_lo > ctx_steps ? (s_lo - ctx_steps) * STEP : 0u,
                                  s_hi > ctx_steps ? min((s_hi - ctx_steps) * STEP, w.n_new) : 0u);
     }
 }
@@ -747,6 +761,7 @@ __global__ __launch_bounds__(kWave * kManyWaves, 2) void k_attend_many(AttnArgs 
     constexpr uint32_t kRowsWg = 16u * MR * kManyWaves;
     extern __shared__ __align__(16) uint32_t smem[];
     __shared__ uint32_t odd_values;  // an infinity or NaN among the drafted values
+    __shared__ bool weighed[kRowsWg];
     const uint32_t lane = lane_id(), wib = uniform(threadIdx.x / kWave);
     const uint32_t col = lane & 15u, g = lane >> 4;
 
@@ -882,12 +897,13 @@ __global__ __launch_bounds__(kWave * kManyWaves, 2) void k_attend_many(AttnArgs 
 #pragma unroll
             for (int n = 0; n < DN; ++n)
                 put_result<E, D>(c, w.split, row, head, 16 * n + 4 * g, rows.o[t][n], rows.m[t], l);
+            if (g == 0) weighed[(wib * MR + t) * 16u + col] = has_weight(l);
         }
     }
     if (ballot(odd) && lane == 0) odd_values = 1;
     __syncthreads();
     if (odd_values)
-        add_odd_values<E, D>(a, w, kRowsWg, s_lo > ctx_steps ? (s_lo - ctx_steps) * STEP : 0u,
+        add_odd_values<E, D>(a, w, kRowsWg, weighed, s_lo > ctx_steps ? (s_lo - ctx_steps) * STEP : 0u,
                              s_hi > ctx_steps ? min((s_hi - ctx_steps) * STEP, w.n_new) : 0u);
 }
 
@@ -937,10 +953,8 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a) {
         }
     }
     for (int o = W / 2; o > 0; o >>= 1) ll += __shfl_xor(ll, o);
-    const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
-    const u32x2 y = {E::pack(x[0] * inv, x[1] * inv), E::pack(x[2] * inv, x[3] * inv)};
-    *reinterpret_cast<u32x2*>(a.out + rh * D + d) = y;
-    if (d == 0 && a.lse) a.lse[rh] = ll > 0.f || ll != ll ? (mm + __builtin_amdgcn_logf(ll)) * kLn2 : -__builtin_inff();
+    *reinterpret_cast<u32x2*>(a.out + rh * D + d) = row_of<E>(x, ll);
+    if (d == 0 && a.lse) a.lse[rh] = has_weight(ll) ? (mm + __builtin_amdgcn_logf(ll)) * kLn2 : -__builtin_inff();
 }
 
 // Shape of a launch, chosen by the host (plan_attention).
