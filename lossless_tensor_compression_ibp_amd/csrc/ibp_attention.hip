@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <limits>
 
 #include "../../include/ibp.h"
 #include "ibp_attention.hpp"
@@ -110,8 +111,9 @@ ibp_status fill_args(const ibp_pages* k, const ibp_pages* v, const ibp_attention
     x->splits = p.splits;
     x->row_tiles = p.row_tiles;
     x->work = (uint32_t)(items * a->n_kv_heads);
-    // a scale of zero weighs all keys alike; masked scores stay -infinity
-    x->scale2 = std::max(std::fabs(a->scale) * kLog2e, 1e-30f);
+    // a scale of zero weighs all keys alike: the smallest number of 32 bits
+    // leaves scores below 1e-6, and masked ones -infinity
+    x->scale2 = std::max(std::fabs(a->scale) * kLog2e, std::numeric_limits<float>::denorm_min());
     x->q_sign = a->scale < 0.f ? 0x80008000u : 0u;
     // Tables in LDS where they fit; large ones otherwise stay in device memory
     // (small ones, of fewer than four positions, always fit).
