@@ -353,6 +353,9 @@ ibp_status ibp_pages_compact(ibp_meta_t meta, void* slots, uint64_t n_slots, uin
  * lies in a page behind a sequence's last token, and keys and values that a
  * row does not see, never reach its result, infinities and NaN included.
  *
+ * Errors are latched on the keys' handle; those of the values' pages and of
+ * the ids in their table on the values' handle as well.
+ *
  * A call is one launch of at most 2^24 - 1 workgroups, one or more for each
  * (row, or sequence of drafted tokens; key/value head); larger ones return
  * IBP_ERR_UNSUPPORTED before anything is queued and are given in parts.

@@ -167,6 +167,14 @@ __device__ __forceinline__ ArgsPtr args_again() {
     return p;
 }
 
+// An error of the keys' pages, or of the values': those are latched on both
+// handles, so that the keys' one stands for the whole call.
+__device__ __forceinline__ void latch_page_error(bool values, uint32_t error) {
+    const ArgsPtr c = args_again();
+    atomicCAS(c->k.err, 0u, error);
+    if (values) atomicCAS(c->v.err, 0u, error);
+}
+
 // What a workgroup works on.
 struct Work {
     uint32_t split, h, item, rt;           // split, key/value head, sequence (tree) or row, row tile
@@ -559,7 +567,7 @@ __global__ __launch_bounds__(kWave * kFewWaves, 2) void k_attend_few(AttnArgs a)
                 const uint32_t k_word = c->k.bitmask[id_k >> 5], v_word = c->v.bitmask[id_v >> 5];
                 comp = (k == kNoPage ? 0u : (k_word >> (id_k & 31u)) & 1u) |
                        (v == kNoPage ? 0u : ((v_word >> (id_v & 31u)) & 1u) << 1);
-                if (k == kNoPage || v == kNoPage) atomicCAS(c->k.err, 0u, (uint32_t)kErrRange);
+                if (k == kNoPage || v == kNoPage) latch_page_error(v == kNoPage, kErrRange);
             }
         }
     };
@@ -595,7 +603,7 @@ __global__ __launch_bounds__(kWave * kFewWaves, 2) void k_attend_few(AttnArgs a)
                                         [&](uint32_t at, u32x4 x) __attribute__((always_inline)) {
                                             put_words<D>(tile + p * T * stride, stride, n, at, x);
                                         }))
-                latch_error(args_again()->k.err, kErrCorrupt);
+                if (lane == 0) latch_page_error(values, kErrCorrupt);
         }
         lds_order();
     };
@@ -801,7 +809,7 @@ __global__ __launch_bounds__(kWave * kManyWaves, 2) void k_attend_many(AttnArgs 
             const uint32_t k_word = c->k.bitmask[id_k >> 5], v_word = c->v.bitmask[id_v >> 5];
             comp = (k == kNoPage ? 0u : (k_word >> (id_k & 31u)) & 1u) |
                    (v == kNoPage ? 0u : ((v_word >> (id_v & 31u)) & 1u) << 1);
-            if (k == kNoPage || v == kNoPage) atomicCAS(c->k.err, 0u, (uint32_t)kErrRange);
+            if (k == kNoPage || v == kNoPage) latch_page_error(v == kNoPage, kErrRange);
         }
     };
     u32x4 st_a[NV], st_b[S::BOTH ? NV : 1];
@@ -840,7 +848,7 @@ __global__ __launch_bounds__(kWave * kManyWaves, 2) void k_attend_many(AttnArgs 
                                         [&](uint32_t at, u32x4 x) __attribute__((always_inline)) {
                                             put_words<D>(to, stride, held, at, x);
                                         }))
-                latch_error(args_again()->k.err, kErrCorrupt);
+                if (lane == 0) latch_page_error(values, kErrCorrupt);
         } else {
             put_raw_page<D, T, NV>(st, to, stride, held);
         }

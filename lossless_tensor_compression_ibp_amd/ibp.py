@@ -624,7 +624,8 @@ def ibp_tree_attention(k: Pages, v: Pages, q: torch.Tensor, k_table: torch.Tenso
     """Attention of drafted tokens (rows new_rows[s] .. new_rows[s + 1] of q,
     k_new, v_new) over their sequence's pages and over the drafted tokens whose
     bits their mask row (int64 words) has.  One token per sequence with mask 1
-    is a decoding step."""
+    is a decoding step.  ibp_check of k's handle has the call's errors, that of
+    v's handle those of the values' pages and ids."""
     a = _queries(q, k_table, _outputs(q, out, lse, k, v), scale)
     if v_table.shape != k_table.shape or v_table.dtype != torch.int64:
         raise ValueError("the block tables of keys and values differ in shape or type")
@@ -697,7 +698,8 @@ def ibp_sparse_attention(k: Pages, v: Pages, q: torch.Tensor, k_table: torch.Ten
                          lens: torch.Tensor, blocks: torch.Tensor, out: torch.Tensor,
                          lse: torch.Tensor | None = None, *, scale: float, row_seq: torch.Tensor | None = None,
                          workspace=None, stream=None):
-    """Attention of each row over the pages that `blocks` lists for it."""
+    """Attention of each row over the pages that `blocks` lists for it.  Errors
+    as in ibp_tree_attention."""
     a = _queries(q, k_table, _outputs(q, out, lse, k, v), scale)
     if v_table.shape != k_table.shape or v_table.dtype != torch.int64:
         raise ValueError("the block tables of keys and values differ in shape or type")
