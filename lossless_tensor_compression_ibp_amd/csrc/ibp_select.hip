@@ -164,6 +164,11 @@ constexpr uint32_t kWaveBlocks = 64;
 // rounding towards zero inside the matrix cores); the products are exact.
 __host__ __device__ constexpr float sum_error(int dim) { return (float)dim / 4194304.0f; }
 
+// And beside that: products and sums below the normal range of 32 bits may be
+// off by as much as its smallest number (in 64 bits such a sum is a score of
+// its own).
+__host__ __device__ constexpr float sum_underflow(int dim) { return (float)dim * 0x1p-125f; }
+
 // Sums of absolute values from here on may overflow in another order.
 constexpr float kLargestSum = 1e38f;
 
@@ -613,6 +618,21 @@ __device__ __forceinline__ uint32_t exact_key(const SelectArgs& a, uint64_t r, u
     return order_of(best);
 }
 
+// Whether the queries of (row r, head h) have a number that is not zero.
+template <int D>
+__device__ __forceinline__ bool any_number(const SelectArgs& a, uint64_t r, uint32_t h, ChooseShared& sh,
+                                           uint32_t& turn) {
+    uint32_t any = 0, zero = 0;
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < a.group * (D / 8); i += blockDim.x) {
+        const u32x4 x = load_eight(static_cast<const uint16_t*>(a.q) + (int64_t)r * a.q_row +
+                                   (int64_t)(h * a.group + i / (D / 8)) * a.q_head + 8 * (i % (D / 8)));
+        any |= (x[0] | x[1] | x[2] | x[3]) & 0x7FFF7FFFu;
+    }
+    choose_max2(any, zero, sh, turn);
+    return any != 0;
+}
+
 template <class E, int D, bool KEYS>
 __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared& sh, uint32_t* smem) {
     uint32_t* const near_words = smem;  // blocks to be summed in 64 bits
@@ -672,6 +692,8 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
         uint32_t slack_bits = __float_as_uint(slack), zero = 0;
         choose_max2(slack_bits, zero, sh, turn);  // (and the keys are in LDS)
         slack = sum_error(D) * __uint_as_float(slack_bits);
+        // (rows of zeros, as a batch is padded with, have no products at all)
+        if (slack_bits != 0 || any_number<D>(a, r, h, sh, turn)) slack += sum_underflow(D);
         const uint32_t own_at = max(at, f_end), own_end = min(end, l_begin);
         auto own = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll 1
@@ -780,7 +802,7 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
                 }
             }
         } else {
-            // no slack (all products zero): the sums as they are
+            // no slack (a row of zeros): the sums, zeros all
             cut = nth_largest(want, lo, hi, sh, turn, &above, own_keys);
             ties = want - above;
         }
