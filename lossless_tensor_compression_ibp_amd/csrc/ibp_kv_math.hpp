@@ -13,6 +13,7 @@ namespace ibp {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 template <class To, class From>
 __device__ __forceinline__ To bits_as(const From& x) {

@@ -11,7 +11,8 @@
 //   1. k_scores multiplies on the matrix cores in 32 bits, and a second
 //      product of the absolute values bounds how far each sum can be off;
 //   2. k_choose finds the n-th largest of these, roughly, and sums again in 64
-//      bits only the pages that lie within that bound of it, usually a few.
+//      bits only the pages that lie within that bound of it, usually a few,
+//      and those whose 32-bit sums say nothing (infinities, NaN, overflow).
 // The result is the one that 64-bit sums of all pages give.  Short rows with
 // pages of their own take both steps in one launch, k_select.
 #include <hip/hip_runtime.h>
@@ -172,6 +173,19 @@ __host__ __device__ constexpr float sum_underflow(int dim) { return (float)dim *
 // Sums of absolute values from here on may overflow in another order.
 constexpr float kLargestSum = 1e38f;
 
+__device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+// The score m of a block whose absolute values sum up to e, as it is stored:
+// NaN where e says nothing of it, being infinite, nearly so, or a NaN (an
+// infinity, a NaN in the bounds, an overflow of 32 bits): k_choose sums such
+// blocks in 64 bits before it does anything else.  Other blocks' e counts for
+// the row's slack.
+__device__ __forceinline__ void settle(float& m, float e, float& slack) {
+    const bool known = e < kLargestSum;
+    m = known ? m : __builtin_nanf("");
+    slack = fmaxf(slack, known ? e : 0.f);
+}
+
 // Blocks of row r (0 where its sequence or length is not valid).
 __device__ __forceinline__ uint32_t row_blocks(const SelectArgs& a, uint64_t r, int64_t* seq) {
     *seq = a.row_seq ? (int64_t)a.row_seq[r] : (int64_t)r;
@@ -230,8 +244,11 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
         const uint32_t b_end = min(nb, b_first + kWaveBlocks * a.span);
         const uint32_t col_tiles = a.head_tiles * ((a.wave_rows + a.rows_per_tile - 1) / a.rows_per_tile);
         for (uint32_t ct0 = 0; ct0 < col_tiles; ct0 += CT) {
-            // the numbers above zero, and those below, of each column
+            // the numbers above zero, and those below, of each column; a head
+            // with a NaN, whose scores are all the lowest, becomes zeros and no
+            // column's head
             V8 qp[CT][DK], qm[CT][DK];
+            uint32_t with_nan[CT];
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 const uint32_t x = (ct0 + c) * 16 + col;  // column of the wave
@@ -239,15 +256,26 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
                 const bool on = head < a.group && row < a.wave_rows && ((mine >> (row & 63u)) & 1u);
                 const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)(r0 + row) * a.q_row +
                                     (int64_t)(h * a.group + head) * a.q_head;
+                u32x4 v[DK];
+                u16x2 top = {0, 0};
 #pragma unroll
                 for (int kk = 0; kk < DK; ++kk) {
-                    const u32x4 v = on ? load_eight(q + 32 * kk + 8 * g) : u32x4{0u, 0u, 0u, 0u};
+                    v[kk] = on ? load_eight(q + 32 * kk + 8 * g) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        top = __builtin_elementwise_max(top, bits_as<u16x2>(v[kk][j] & 0x7FFF7FFFu));
+                }
+                const uint64_t nan = ballot(top.x > E::kExponent || top.y > E::kExponent);
+                with_nan[c] = (uint32_t)((nan | nan >> 16 | nan >> 32 | nan >> 48) & 0xFFFFu);
+                const uint32_t keep = ((with_nan[c] >> col) & 1u) - 1u;
+#pragma unroll
+                for (int kk = 0; kk < DK; ++kk) {
                     u32x4 p, m;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint32_t neg = (v[j] >> 15 & 0x10001u) * 0xFFFFu;
-                        p[j] = v[j] & ~neg;
-                        m[j] = v[j] & neg;
+                        const uint32_t x = v[kk][j] & keep, neg = (x >> 15 & 0x10001u) * 0xFFFFu;
+                        p[j] = x & ~neg;
+                        m[j] = x & neg;
                     }
                     qp[c][kk] = bits_as<V8>(p);
                     qm[c][kk] = bits_as<V8>(m);
@@ -264,7 +292,8 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t row = (x0 + i) >> a.log2_pad;
-                    if (x0 + i - (row << a.log2_pad) < a.group) heads[c] |= 1u << i;
+                    if (x0 + i - (row << a.log2_pad) < a.group && !((with_nan[c] >> (4 * g + i)) & 1u))
+                        heads[c] |= 1u << i;
                     if (i < ROWS) {
                         const bool live = row < a.wave_rows && ((mine >> (row & 63u)) & 1u);
                         const uint32_t n = (uint32_t)__shfl((int)my_nb, (int)(row & 63u));
@@ -341,28 +370,25 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
                             // a NaN is left out: fmaxf takes its other argument
                             v[i] = (heads[c] >> i) & 1u ? fmaxf(s[i], -__builtin_inff()) : -__builtin_inff();
                             w[i] = wp[i] - wm[i];
-                            // infinite or NaN (an infinite bound, a NaN in q or the
-                            // bounds, an overflow of 32 bits or nearly one): nothing
-                            // is known of the score, and every page is near
-                            w[i] = w[i] < kLargestSum ? fmaxf(w[i], 0.f) : __builtin_inff();
                         }
                         if constexpr (ONE_ROW) {
                             float m = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-                            float e = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+                            float e = max_or_nan(max_or_nan(w[0], w[1]), max_or_nan(w[2], w[3]));
                             if (a.pad >= 8) {
                                 m = fmaxf(m, __shfl_xor(m, 16));
-                                e = fmaxf(e, __shfl_xor(e, 16));
+                                e = max_or_nan(e, __shfl_xor(e, 16));
                             }
                             if (a.pad >= 16) {
                                 m = fmaxf(m, __shfl_xor(m, 32));
-                                e = fmaxf(e, __shfl_xor(e, 32));
+                                e = max_or_nan(e, __shfl_xor(e, 32));
                             }
                             if (b < row_nb[c][0]) {
-                                slack[c] = fmaxf(slack[c], e);
+                                settle(m, e, slack[c]);
                                 const bool later = a.head_tiles > 1 && ct0 + c > 0;
                                 if (x0 == (row0 << a.log2_pad) || (later && g == 0)) {
                                     float* to = a.scores + ((r0 + row0) * a.kv_heads + h) * a.pitch + b;
-                                    if (later) m = fmaxf(m, *to);  // a row of several tiles: the highest so far
+                                    // a row of several tiles: the highest so far, or a NaN
+                                    if (later) m = max_or_nan(m, *to);
                                     *to = m;
                                 }
                             }
@@ -370,10 +396,10 @@ __device__ __forceinline__ void score_blocks(const SelectArgs& a, uint64_t r0, u
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 if (a.pad == 2 && (i & 1)) continue;
-                                const float m = a.pad == 2 ? fmaxf(v[i], v[i | 1]) : v[i];
-                                const float e = a.pad == 2 ? fmaxf(w[i], w[i | 1]) : w[i];
+                                float m = a.pad == 2 ? fmaxf(v[i], v[i | 1]) : v[i];
+                                const float e = a.pad == 2 ? max_or_nan(w[i], w[i | 1]) : w[i];
                                 if (b < row_nb[c][i]) {
-                                    slack[c] = fmaxf(slack[c], e);
+                                    settle(m, e, slack[c]);
                                     a.scores[((r0 + ((x0 + i) >> a.log2_pad)) * a.kv_heads + h) * a.pitch + b] = m;
                                 }
                             }
@@ -582,6 +608,12 @@ __device__ __forceinline__ uint32_t nth_largest(uint32_t want, uint32_t lo, uint
     return lo + (prefix >> lz);
 }
 
+// max(y lo, y hi), or a NaN of either.
+__device__ __forceinline__ double larger_product(double y, double lo, double hi) {
+    const double to_lo = y * lo, to_hi = y * hi;
+    return to_lo != to_lo || to_lo > to_hi ? to_lo : to_hi;
+}
+
 // One wave: the score of page b of (row r, head h) summed in 64 bits, as a
 // key.  Sixteen lanes take a query head, eight dims each at a time.
 template <class E, int D>
@@ -603,10 +635,7 @@ __device__ __forceinline__ uint32_t exact_key(const SelectArgs& a, uint64_t r, u
                 for (int e = 0; e < 8; ++e) {
                     const int sh = 16 * (e & 1);
                     const double y = (double)E::from_bits(x[e >> 1] >> sh);
-                    const double to_lo = y * (double)E::from_bits(lo[e >> 1] >> sh);
-                    const double to_hi = y * (double)E::from_bits(hi[e >> 1] >> sh);
-                    // the larger, or a NaN of either
-                    s += to_lo != to_lo || to_lo > to_hi ? to_lo : to_hi;
+                    s += larger_product(y, (double)E::from_bits(lo[e >> 1] >> sh), (double)E::from_bits(hi[e >> 1] >> sh));
                 }
             }
         }
@@ -618,16 +647,40 @@ __device__ __forceinline__ uint32_t exact_key(const SelectArgs& a, uint64_t r, u
     return order_of(best);
 }
 
-// Whether the queries of (row r, head h) have a number that is not zero.
-template <int D>
+// One thread: the same, for the rare pages of which a 32-bit sum says nothing.
+// Rolled up, so that it takes few registers.
+template <class E, int D>
+__device__ __forceinline__ uint32_t lone_key(const SelectArgs& a, uint64_t r, uint32_t h, const uint16_t* bounds) {
+    float best = -__builtin_inff();
+#pragma unroll 1
+    for (uint32_t j = 0; j < a.group; ++j) {
+        const uint16_t* q =
+            static_cast<const uint16_t*>(a.q) + (int64_t)r * a.q_row + (int64_t)(h * a.group + j) * a.q_head;
+        double s = 0.0;
+#pragma unroll 2
+        for (int d = 0; d < D; ++d) {
+            const double y = (double)E::from_bits(q[d]);
+            s += larger_product(y, (double)E::from_bits(bounds[d]), (double)E::from_bits(bounds[D + d]));
+        }
+        best = fmaxf(best, (float)s);
+    }
+    return order_of(best);
+}
+
+// Whether a head of (row r, key/value head h) has a number that is not zero,
+// and no NaN.  A wave takes a head at a time.
+template <class E, int D>
 __device__ __forceinline__ bool any_number(const SelectArgs& a, uint64_t r, uint32_t h, ChooseShared& sh,
                                            uint32_t& turn) {
     uint32_t any = 0, zero = 0;
 #pragma unroll 1
-    for (uint32_t i = threadIdx.x; i < a.group * (D / 8); i += blockDim.x) {
-        const u32x4 x = load_eight(static_cast<const uint16_t*>(a.q) + (int64_t)r * a.q_row +
-                                   (int64_t)(h * a.group + i / (D / 8)) * a.q_head + 8 * (i % (D / 8)));
-        any |= (x[0] | x[1] | x[2] | x[3]) & 0x7FFF7FFFu;
+    for (uint32_t j = threadIdx.x / kWave; j < a.group; j += blockDim.x / kWave) {
+        const uint16_t* q =
+            static_cast<const uint16_t*>(a.q) + (int64_t)r * a.q_row + (int64_t)(h * a.group + j) * a.q_head;
+        uint32_t top = 0;
+#pragma unroll 1
+        for (uint32_t d = lane_id(); d < (uint32_t)D; d += kWave) top = max(top, q[d] & 0x7FFFu);
+        if (ballot(top != 0) != 0 && ballot(top > E::kExponent) == 0) any = 1;
     }
     choose_max2(any, zero, sh, turn);
     return any != 0;
@@ -692,9 +745,15 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
         uint32_t slack_bits = __float_as_uint(slack), zero = 0;
         choose_max2(slack_bits, zero, sh, turn);  // (and the keys are in LDS)
         slack = sum_error(D) * __uint_as_float(slack_bits);
-        // (rows of zeros, as a batch is padded with, have no products at all)
-        if (slack_bits != 0 || any_number<D>(a, r, h, sh, turn)) slack += sum_underflow(D);
+        // (rows of zeros or NaNs, as a batch may be padded with, have no products)
+        if (slack_bits != 0 || any_number<E, D>(a, r, h, sh, turn)) slack += sum_underflow(D);
         const uint32_t own_at = max(at, f_end), own_end = min(end, l_begin);
+        const int64_t* table = a.table + ((uint64_t)seq * a.kv_heads + h) * a.blocks;
+        const uint16_t* bounds = static_cast<const uint16_t*>(a.bounds);
+        auto bounds_of = [&](uint32_t b) __attribute__((always_inline)) {
+            const uint32_t id = page_id(table[b], (uint32_t)a.n_slots);
+            return bounds + (uint64_t)(id == kNoPage ? 0u : id) * (2ull * D);
+        };
         auto own = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll 1
             for (uint32_t b = own_at; b < own_end; ++b) f(b, key_of(b));
@@ -702,12 +761,37 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
         auto own_keys = [&](auto f) __attribute__((always_inline)) {
             own([&](uint32_t, uint32_t k) __attribute__((always_inline)) { f(k); });
         };
-        uint32_t not_lo = 0, hi = 0;
-        own_keys([&](uint32_t k) __attribute__((always_inline)) {
-            not_lo = max(not_lo, ~k);
-            hi = max(hi, k);
-        });
-        choose_max2(not_lo, hi, sh, turn);
+        uint32_t not_lo, hi;
+        auto range_of = [&](auto each) __attribute__((always_inline)) {
+            not_lo = hi = 0;
+            each([&](uint32_t k) __attribute__((always_inline)) {
+                not_lo = max(not_lo, ~k);
+                hi = max(hi, k);
+            });
+            choose_max2(not_lo, hi, sh, turn);
+        };
+        range_of(own_keys);
+        // Pages with key 0, a NaN: nothing is known of them yet.  A thread sums
+        // its own in 64 bits if no thread has more than two; else all pages
+        // are near.
+        bool unbounded = false;
+        if (not_lo == 0xFFFFFFFFu) {
+            uint32_t mine = 0, zero2 = 0;
+            own_keys([&](uint32_t k) __attribute__((always_inline)) { mine += k == 0; });
+            choose_max2(mine, zero2, sh, turn);
+            unbounded = mine > 2;
+            if (!unbounded) {
+                own([&](uint32_t b, uint32_t k) __attribute__((always_inline)) {
+                    if (k != 0) return;
+                    k = lone_key<E, D>(a, r, h, bounds_of(b));
+                    if (KEYS)
+                        keys[b] = k;
+                    else
+                        scores[b] = value_of(k);
+                });
+                range_of(own_keys);
+            }
+        }
         const uint32_t lo = ~not_lo;
         // One pass: the bin of kBins between lo and hi that holds the want-th
         // largest sum.  Keys of scores that lie close together differ in
@@ -719,15 +803,13 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
         });
         const float t_lo = value_of(lo + (bin << drop));
         const float t_hi = value_of(min(hi, lo + (bin << drop) + ((1u << drop) - 1)));
-        if (slack > 0.f) {
+        if (slack > 0.f || unbounded) {
             // Every true score is within `slack` of its sum, so the want-th
             // largest true one lies between t_lo and t_hi widened by slack;
             // pages that are further than two of them outside are decided
             // (a third covers the roundings of these bounds and of the score).
-            // An infinite slack (kLargestSum) decides none.
-            const bool bounded = slack < __builtin_inff();
-            const uint32_t near_lo = order_of(bounded ? t_lo - 3.f * slack : -__builtin_inff());
-            const uint32_t near_hi = order_of(bounded ? t_hi + 3.f * slack : __builtin_inff());
+            const uint32_t near_lo = unbounded ? 0u : order_of(t_lo - 3.f * slack);
+            const uint32_t near_hi = unbounded ? 0xFFFFFFFFu : order_of(t_hi + 3.f * slack);
             uint32_t n_above = 0, n_near = 0;
             own([&](uint32_t b, uint32_t k) __attribute__((always_inline)) {
                 if (k > near_hi) {
@@ -744,16 +826,12 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
             if (n.all[0] + n.all[1] == want) {
                 cut = near_lo - 1;  // the near ones are exactly those still wanted
             } else {
-                const int64_t* table = a.table + ((uint64_t)seq * a.kv_heads + h) * a.blocks;
-                const uint16_t* bounds = static_cast<const uint16_t*>(a.bounds);
                 const uint32_t rest = want - n.all[0];
                 marked = true;
                 if (n.all[1] <= kNearList) {
                     // the usual case: a few, in a list, ranked by one wave
                     for (uint32_t i = wib; i < n.all[1]; i += nt / kWave) {
-                        const uint32_t id = page_id(table[uniform(sh.near_block[i])], (uint32_t)a.n_slots);
-                        const uint32_t k =
-                            exact_key<E, D>(a, r, h, bounds + (uint64_t)(id == kNoPage ? 0u : id) * (2ull * D));
+                        const uint32_t k = exact_key<E, D>(a, r, h, bounds_of(uniform(sh.near_block[i])));
                         if (lane == 0) sh.near_key[i] = k;
                     }
                     __syncthreads();
@@ -773,9 +851,7 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
                     for (uint32_t w = wib; w < (nb + 31) / 32; w += nt / kWave) {
                         for (uint32_t m = uniform(near_words[w]); m; m &= m - 1) {
                             const uint32_t b = 32 * w + (uint32_t)__builtin_ctz(m);
-                            const uint32_t id = page_id(table[b], (uint32_t)a.n_slots);
-                            const uint32_t k =
-                                exact_key<E, D>(a, r, h, bounds + (uint64_t)(id == kNoPage ? 0u : id) * (2ull * D));
+                            const uint32_t k = exact_key<E, D>(a, r, h, bounds_of(b));
                             if (lane == 0) {
                                 if (KEYS)
                                     keys[b] = k;
@@ -791,18 +867,13 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
                             if (is_near(b)) f(k);
                         });
                     };
-                    not_lo = hi = 0;
-                    near_keys([&](uint32_t k) __attribute__((always_inline)) {
-                        not_lo = max(not_lo, ~k);
-                        hi = max(hi, k);
-                    });
-                    choose_max2(not_lo, hi, sh, turn);
+                    range_of(near_keys);
                     cut = nth_largest(rest, ~not_lo, hi, sh, turn, &above, near_keys);
                     ties = rest - above;
                 }
             }
         } else {
-            // no slack (a row of zeros): the sums, zeros all
+            // no slack (a row of zeros or NaNs): the sums, all alike
             cut = nth_largest(want, lo, hi, sh, turn, &above, own_keys);
             ties = want - above;
         }
@@ -1001,10 +1072,11 @@ ibp_status ibp_select_pages(ibp_meta_t h, const ibp_attention* a, const void* q,
     const bool one_launch = scored && !shared && a->table_blocks <= kOneLaunchBlocks;
     const bool keys = a->table_blocks <= kLdsKeys;
     // waves that choose: eight blocks per thread
-    const uint32_t waves =
-        one_launch ? kSelectWaves
-        : keys     ? (uint32_t)std::min<uint64_t>(kMaxChooseWaves, std::max<uint64_t>(4, (a->table_blocks + 8 * kWave - 1) / (8 * kWave)))
-                   : kMaxChooseWaves;
+    uint32_t waves = kMaxChooseWaves;
+    if (one_launch)
+        waves = kSelectWaves;
+    else if (keys)
+        waves = (uint32_t)std::min<uint64_t>(waves, std::max<uint64_t>(4, (a->table_blocks + 8 * kWave - 1) / (8 * kWave)));
     if (a->n_rows * a->n_kv_heads > max_workgroups(kWave * waves) || (scored && !one_launch && groups > 65535))
         return IBP_ERR_UNSUPPORTED;
     auto launch = [&](auto e, auto dc) {
