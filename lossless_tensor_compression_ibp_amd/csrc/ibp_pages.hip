@@ -617,10 +617,9 @@ ibp_status ibp_pages_compact(ibp_meta_t h, void* slots, uint64_t n_slots, uint32
                              int64_t* map, int64_t* n_live, int64_t* table, uint64_t n_entries, void* workspace,
                              uint64_t workspace_bytes, hipStream_t stream) {
     if (!h) return IBP_ERR_INVALID_ARG;
-    if (n_slots == 0) return IBP_OK;
     DeviceGuard guard(h->device);
     if (!guard.ok) return IBP_ERR_DEVICE;
-    if (n_slots > kMaxPoolSlots || n_entries > 1ull << 62) return IBP_ERR_INVALID_ARG;
+    if (n_slots == 0 || n_slots > kMaxPoolSlots || n_entries > 1ull << 62) return IBP_ERR_INVALID_ARG;
     if (!device_or_pinned(slots, h->device)) return IBP_ERR_INVALID_ARG;
     for (const void* p : {(const void*)bitmask, (const void*)refs, (const void*)map, (const void*)n_live})
         if (!device_only(p, h->device)) return IBP_ERR_INVALID_ARG;
