@@ -1300,12 +1300,19 @@ static hipError_t launch_tiles(const Tables& t, const Geo& geo, const void* slot
                                uint32_t* err, hipStream_t s) {
     // the record (up to the slot) and the zero word after it
     const uint32_t lds_words = (uint32_t)geo.n_words + 8;
-    const dim3 grid((uint32_t)((n_out + kWavesPerBlock - 1) / kWavesPerBlock));
     const dim3 block(kWave * kWavesPerBlock);
     const size_t shm = (size_t)lds_words * 4 * kWavesPerBlock;
-    hipLaunchKernelGGL((k_decode_tiles<RUNS, UNI>), grid, block, shm, s, t, geo, static_cast<const uint8_t*>(slots),
-                       n_slots, bitmask, ids, n_out, static_cast<uint8_t*>(dst), err, lds_words);
-    return hipGetLastError();
+    for (uint64_t at = 0; at < n_out; at += kRowsPerLaunch) {
+        const uint64_t n = min(n_out - at, kRowsPerLaunch);
+        const uint64_t skip = ids ? 0 : at;  // without ids, row i is slot i
+        hipLaunchKernelGGL((k_decode_tiles<RUNS, UNI>), dim3((uint32_t)((n + kWavesPerBlock - 1) / kWavesPerBlock)),
+                           block, shm, s, t, geo, static_cast<const uint8_t*>(slots) + skip * geo.L, n_slots - skip,
+                           bitmask + skip / 32, ids ? ids + at : nullptr, n, static_cast<uint8_t*>(dst) + at * geo.L,
+                           err, lds_words);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // Tensors longer than one tile: one wave per group of tiles; lb holds one

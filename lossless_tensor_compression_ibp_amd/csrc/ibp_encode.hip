@@ -1119,8 +1119,14 @@ static hipError_t launch_encode_r(const Tables& t, const Geo& geo, bool uniform_
                                                                        s, &launched);
             if (e != hipSuccess || launched) return e;
         }
-        return launch_encode_t<false>(t, geo, RUNS, src, n_tensors, slots, bitmask, stored, LookBack{}, lds_words,
-                                      s);
+        for (uint64_t at = 0; at < n_tensors; at += kRowsPerLaunch) {
+            const hipError_t e = launch_encode_t<false>(
+                t, geo, RUNS, static_cast<const uint8_t*>(src) + at * geo.L, min(n_tensors - at, kRowsPerLaunch),
+                static_cast<uint8_t*>(slots) + at * geo.L, bitmask + at / 32, stored ? stored + at : nullptr, LookBack{},
+                lds_words, s);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
     }
     hipError_t e = encode_two_pass(geo)
                        ? launch_encode_groups<RUNS>(t, geo, uniform_meta, src, n_tensors, slots, *lb, s)

@@ -148,6 +148,13 @@ inline uint64_t encode_status_words(const Geo& g, uint64_t n_tensors) {
 // in `bits` (in place; gpt consecutive groups per tensor).
 hipError_t launch_group_scan(uint64_t n_tensors, uint64_t gpt, uint64_t base, uint64_t* bits, hipStream_t s);
 
+// Threads of one launch along a dimension of its grid.  The runtime does not
+// refuse more: it takes the number modulo 2^32 and runs those.
+constexpr uint64_t kMaxLaunchThreads = 0xFFFFFFFFull;
+constexpr uint64_t max_workgroups(uint64_t threads) { return kMaxLaunchThreads / threads; }
+// Rows per launch of the kernels that take a wave each: whole bitmask words.
+constexpr uint64_t kRowsPerLaunch = 1ull << 25;
+
 enum DeviceError : uint32_t { kErrNone = 0, kErrCorrupt = 5, kErrRange = 6, kErrStall = 7, kErrFull = 8 };
 
 // Where tensor t's stored item lives.  offsets == nullptr: fixed slots, slot
