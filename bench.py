@@ -58,26 +58,29 @@ def _code_only(text: str) -> str:
     return " ".join(text.split())
 
 
+# What the decode and encode kernels, their tables and their launches are built
+# from (the page operators' sources are not among them).
+CODEC_SOURCES = ("ibp_api.hip", "ibp_decode.hip", "ibp_device.hpp", "ibp_encode.hip", "ibp_host.hpp",
+                 "ibp_internal.hpp", "ibp_meta.hip")
+
+
 def kernel_source_hash() -> str:
-    """Hash of the kernel sources' code (comments and layout ignored); counter
-    readings in profiles/traffic.json apply only while it matches."""
-    import glob
+    """Hash of the codec's kernel sources' code (comments and layout ignored);
+    counter readings in profiles/traffic.json apply only while it matches."""
     import hashlib
 
     csrc = os.path.join(ROOT, "lossless_tensor_compression_ibp_amd", "csrc")
-    files = sorted(glob.glob(os.path.join(csrc, "*.hip")) + glob.glob(os.path.join(csrc, "*.hpp")))
-    files.append(os.path.join(ROOT, "include", "ibp.h"))
     h = hashlib.sha256()
-    for f in sorted(files, key=os.path.basename):
-        h.update(os.path.basename(f).encode())
-        with open(f, encoding="utf-8") as fh:
+    for name in CODEC_SOURCES:
+        h.update(name.encode())
+        with open(os.path.join(csrc, name), encoding="utf-8") as fh:
             h.update(_code_only(fh.read()).encode())
     return h.hexdigest()[:16]
 
 
 TRAFFIC_SOURCE = ("copied from profiles/traffic.json: rocprofv3 --pmc FETCH_SIZE and --pmc WRITE_SIZE of a separate "
                   "run of this workload (KiB per dispatch, one counter per run), each scaled by what the counter "
-                  "reads for a copy of known size with the same access pattern; null when the kernel sources changed "
+                  "reads for a copy of known size with the same access pattern; null when the codec's sources changed "
                   "since the counters were taken")
 TRAFFIC_SUMS_LINK = ("bytes per launch: reads over the host link (whole 128-byte lines) + HBM reads of ids, bitmask and "
                      "header words + HBM writes of the decoded rows")
