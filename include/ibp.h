@@ -376,9 +376,9 @@ typedef struct ibp_attention {
     uint32_t n_q_heads;
     uint32_t n_kv_heads;
     float scale;
-    uint64_t n_rows;         /* rows of q, out and lse */
-    uint64_t n_seqs;         /* rows of the block tables: n_seqs x n_kv_heads x table_blocks */
-    uint64_t table_blocks;
+    uint64_t n_rows;         /* rows of q, out and lse; without any a call does nothing */
+    uint64_t n_seqs;         /* rows of the block tables: n_seqs x n_kv_heads x table_blocks, */
+    uint64_t table_blocks;   /* at least 1 each where there are rows */
     uint64_t max_len;        /* about the longest context: a hint, read to plan the split only */
     uint32_t max_new;        /* most drafted tokens of a sequence (tree attention) */
     int64_t q_row_stride, q_head_stride;
@@ -415,22 +415,25 @@ ibp_status ibp_tree_attention(const ibp_pages* k, const ibp_pages* v, const ibp_
 ibp_status ibp_page_bounds(const ibp_pages* k, uint32_t dtype, uint32_t head_dim, const int64_t* ids,
                            const int32_t* tokens, uint64_t n, void* bounds, hipStream_t stream);
 
-/* The pages that each query reads: row r of q belongs to sequence
- * row_seq[r] (device int32; NULL: r) and sees its first lens[r] tokens, in
- * nb = ceil(lens[r] / page_tokens) pages.  blocks (device int32, n_rows x
- * n_kv_heads x n_blocks) receives block numbers in ascending order, -1 behind
- * them: the first keep_first and the last keep_last of the nb, then those
- * with the highest score until there are n_blocks.  A block's score is the
- * highest of its bound over the query heads of the group, summed in 64 bits
- * and rounded to 32; equal scores go to the lower block, and a NaN counts as
- * the lowest (an infinite bound is one like any other: only 0 times infinity
- * and sums of both infinities are NaN).  bounds: pool-wide, as ibp_page_bounds leaves them, indexed by
- * the ids of the keys' table.  At most 2^17 blocks per row and 2^22 - 1 rows
- * times key/value heads.  Rows four times as many as the sequences, in groups
- * of up to 16 query heads: at most 262,140; others in tables of more than 1,024
- * blocks: 65,535.  More may return IBP_ERR_UNSUPPORTED, before anything is
- * queued, and are given in parts.  Of a, max_len,
- * max_new, scale and the new_ strides are not read. */
+/* The pages that each query reads: row r of q belongs to sequence row_seq[r]
+ * (device int32; NULL: r) and sees its first lens[r] tokens, in nb =
+ * ceil(lens[r] / page_tokens) pages.  blocks (device int32, n_rows x n_kv_heads
+ * x n_blocks) receives block numbers in ascending order, -1 behind them: the
+ * first keep_first and the last keep_last of the nb, then those with the
+ * highest score until there are n_blocks.  A block's score is the highest of
+ * its bound over the query heads of the group, summed in 64 bits and rounded to
+ * 32; equal scores go to the lower block, and a NaN counts as the lowest (an
+ * infinite bound is one like any other: only 0 times infinity and sums of both
+ * infinities are NaN).  bounds: pool-wide, as ibp_page_bounds leaves them,
+ * indexed by the ids of the keys' table.
+ *
+ * At most 2^17 blocks per row and 2^22 - 1 rows times key/value heads.  Rows
+ * four times as many as the sequences, in groups of up to 16 query heads: at
+ * most 262,140; others in tables of more than 1,024 blocks: 65,535.  More may
+ * return IBP_ERR_UNSUPPORTED, before anything is queued, and are given in
+ * parts; so are batches whose scratch, about 4 bytes for each row, head and
+ * block, is more than a caller can spare.  Of a, max_len, max_new, scale and
+ * the new_ strides are not read. */
 uint64_t ibp_select_pages_workspace(const ibp_attention* a);
 ibp_status ibp_select_pages(ibp_meta_t meta, const ibp_attention* a, const void* q, const void* bounds,
                             uint64_t n_slots, const int64_t* k_table, const int32_t* lens, const int32_t* row_seq,

@@ -97,7 +97,7 @@ inline ibp_status check_attention(const ibp_attention* a) {
     if (a->head_dim != 64 && a->head_dim != 128 && a->head_dim != 256) return IBP_ERR_UNSUPPORTED;
     if (a->page_tokens != 16 && a->page_tokens != 32 && a->page_tokens != 64) return IBP_ERR_UNSUPPORTED;
     if ((uint64_t)a->head_dim * a->page_tokens * 2 > kMaxPageBytes) return IBP_ERR_UNSUPPORTED;
-    if (a->n_seqs == 0 || a->table_blocks == 0) return IBP_ERR_INVALID_ARG;
+    if (a->n_rows && (a->n_seqs == 0 || a->table_blocks == 0)) return IBP_ERR_INVALID_ARG;
     if (a->table_blocks > (1ull << 31) / a->page_tokens || a->n_seqs > (1ull << 31) || a->n_rows > (1ull << 31))
         return IBP_ERR_INVALID_ARG;
     if (a->q_row_stride < 0 || a->q_head_stride < 0) return IBP_ERR_INVALID_ARG;
