@@ -21,8 +21,8 @@
 //     rows, without a barrier, and the waves' results are joined at the end.
 //     Bound by the pages' bytes, or by latency when there are few of them (16
 //     streams of 4 K and 16 heads of 64 dims, 185 MB: 37 us, 5 TB/s; one of
-//     1,000 tokens and 8 heads of 128 dims: 8.6 us and 3.6 to join; 512 rows
-//     with 128 of 4,096 pages each, 4.3 GB out of the caches: 297 us, 14 TB/s).
+//     1,000 tokens and 8 heads of 128 dims: 9.1 us and 4.0 to join; 512 rows
+//     with 128 of 4,096 pages each, 4.3 GB out of the caches: 284 us, 15 TB/s).
 //   k_attend_many.  Four waves with 16 MR rows each share a step's pages,
 //     which they load and rebuild between them; two such workgroups on a
 //     compute unit overlap one's rebuilding with the other's products.  (Eight
@@ -30,10 +30,11 @@
 //     that rebuild hold up all others; eight streams of 24 drafted tokens over
 //     8 K 140 us instead of 86, two 64 K contexts with 64 drafted tokens,
 //     nothing to rebuild, 470 us instead of 420.)  With the join these now
-//     take 87 and 380 us, the latter 724 TFLOP/s, 0.6 of a large matrix
-//     product: LDS (a step's operands, half of them as transposed 8-byte
-//     reads), the products and the exponentials each work a quarter of the
-//     time, and wait for each other.
+//     take 88 and 379 us in calls queued one after another (405 us each in a
+//     kernel trace), the latter 726 TFLOP/s, 0.6 of a large matrix product:
+//     LDS (a step's operands, half of them as transposed 8-byte reads), the
+//     products and the exponentials each work a quarter of the time, and wait
+//     for each other.
 // A long context is split over workgroups; k_join adds the parts.
 #pragma once
 

@@ -14,10 +14,10 @@
 // ranked by a prefix sum (the lowest first), counts change by integer
 // atomics, and bitmask bits by atomic AND / OR of single bits.
 //
-// Short calls are bound by launches: 263 pages of 4 KiB are copied in 4.3 us
-// on the GPU and 7.2 us of host time per call.  Compacting 65,536 slots of
-// 4 KiB, 55 % of them live, moves 134 MB in 27 us, 5 TB/s, what a large copy
-// reaches; counting, planning and remapping take 13 us more.
+// Short calls are bound by launches: 263 pages of 4 KiB are copied in 4.5 us
+// on the GPU and 7.3 us of host time per call.  Compacting 65,536 slots of
+// 4 KiB, 55 % of them live, moves 134 MB in 35 us, 3.8 TB/s (a large copy
+// 4.8); counting, planning and remapping take 12 us more.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

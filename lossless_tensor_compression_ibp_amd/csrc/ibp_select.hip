@@ -32,8 +32,8 @@ namespace ibp {
 // a power of two of words and at most 256 of them, the same eight dims in
 // every vector.  So a lane keeps its dims' running bounds over its vectors and
 // the lanes of one dim group are joined at the end.  Bound by the pages' bytes
-// (65,536 pages of 4 KiB under a whole-page period: 62.5 us, 4.8 TB/s read and
-// written, what a large copy reaches; 67 pages: 5.5 us, one launch's latency).
+// (65,536 pages of 4 KiB under a whole-page period: 64.3 us, 4.7 TB/s read and
+// written, what a large copy reaches; 67 pages: 4.2 us, one launch's latency).
 // ---------------------------------------------------------------------------
 constexpr uint32_t kBoundWaves = 4;
 
@@ -124,13 +124,13 @@ __global__ __launch_bounds__(kWave * kBoundWaves) void k_page_bounds(Pool pool, 
 //   k_scores, decoding, where every row has pages of its own: CT = 1, other
 //     blocks in every wave, operands straight from memory.  Bound by the
 //     bounds' bytes (16 rows of 2,048 blocks by 8 heads of 128 dims, 134 MB:
-//     20.7 us, 6.5 TB/s out of the last-level cache).
+//     21.6 us, 6.2 TB/s out of the last-level cache).
 //   k_scores_shared, rows that share a sequence: the four waves of a workgroup
 //     take the same blocks for rows of their own, and bring the bounds to LDS
 //     once.  An operand's 16 lanes are 16 pages, so that a load from memory
 //     takes the cache 64 lookups instead of 8: read that way, with each wave
 //     on its own, the cache's one lookup per cycle was the limit (512 rows of
-//     4,096 blocks by 8 heads of 128 dims: 138 us, 79.6 through LDS, of which
+//     4,096 blocks by 8 heads of 128 dims: 138 us, 77 through LDS, of which
 //     the matrix cores work 27).  Workgroups whose rows belong to several
 //     sequences, and 256 dims, which LDS has no room for, still read that way.
 // Heads are the fastest index of the grid, so that with eight of them each
@@ -914,7 +914,7 @@ __device__ __forceinline__ void choose_blocks(const SelectArgs& a, ChooseShared&
 
 // 64 registers for pages of up to 128 dims, so that eight waves fit a SIMD: the
 // 64-bit sums read from everywhere and wait (512 rows of 4,096 blocks on 8
-// heads: 88 us, 124 us with the 94 registers the compiler takes by itself).
+// heads: 86 us, 124 us with the 94 registers the compiler takes by itself).
 // 256 dims would spill.
 template <class E, int D, bool KEYS>
 __global__ __launch_bounds__(1024, D <= 128 ? 8 : 4) void k_choose(SelectArgs a) {
@@ -926,7 +926,8 @@ __global__ __launch_bounds__(1024, D <= 128 ? 8 : 4) void k_choose(SelectArgs a)
 // Both in one launch, for rows with pages of their own in tables of at most
 // kOneLaunchBlocks blocks: the workgroup of a (row, head) scores its blocks,
 // 64 a wave at a time, and chooses among them.  (A row of 256 blocks and 8
-// heads of 128 dims: 8 and 6 us in two launches.)
+// heads of 128 dims: 14 us, as much as the two launches, 8 and 6, without the
+// 4 to 5 us that the second one costs the host.)
 constexpr uint32_t kSelectWaves = 8;
 constexpr uint64_t kOneLaunchBlocks = 1024;
 
